@@ -23,7 +23,8 @@
  *   - Arguments are validated on the host before any launch: a bad shape, pointer or alignment
  *     returns TQ_EINVAL, an unsupported size TQ_EUNSUPPORTED, and nothing is launched.  A launch
  *     failure returns TQ_ECUDA.  tq_last_error() then holds a one-line, thread-local message.
- *   - Input values are not checked: NaN or Inf inputs give undefined outputs.
+ *   - Input values are not checked: NaN or Inf inputs give undefined outputs (the paged-cache calls
+ *     below never read what lies behind a sequence's last token).
  *   - Kernels never trap or assert; out-of-range slots or block-table entries are skipped.
  *   - Outputs are undefined after an error.
  *
@@ -309,6 +310,130 @@ tq_status tq_search_workspace_size(const tq_ctx *ctx, int32_t nq, int64_t n, int
 tq_status tq_search_topk(const tq_ctx *ctx, const void *q, tq_dtype dtype, int32_t nq,
                          tq_packed db, int64_t n, int32_t k, float *out_scores, int64_t *out_idx,
                          void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Paged caches: what a serving loop runs around them.  tq_page_extend makes block tables, lengths
+ * and slot maps on the GPU (the `slots` of tq_encode_kv, the `new_slots` of tq_decode_step);
+ * tq_append_kv, tq_block_scores and tq_attend_paged serve an uncompressed paged cache (the layers
+ * that a user keeps in full precision, [ZC] 第六部分 "Boundary V"); tq_block_scores and
+ * tq_select_blocks choose the blocks that one decode step reads, for tq_attend_paged and for
+ * tq_attend_decode over the compressed cache alike.
+ *
+ * Every cache of a model can share one tq_pages: block e of KV head h, token t % block_size, is slot
+ *   (e * n_kv_heads + h) * block_size + t % block_size,
+ * the slot of tq_attn_desc's paged layout.  An uncompressed cache is a dense array of rows indexed
+ * by slot, [n_blocks][n_kv_heads][block_size][d].
+ *   device       where the work runs (these calls have no context)
+ *   n_blocks     physical blocks; table entries outside [0, n_blocks) name no block: their tokens
+ *                get no slot, are not written, and take no part in attention
+ *   block_table  device int32 [batch][max_blocks]
+ * Supported: batch * n_kv_heads and n_blocks * n_kv_heads up to 2^31 - 1, max_blocks * block_size up
+ * to 2^31 - 1.  Lengths are device int32 [batch]; negative ones count as 0, and those past
+ * max_blocks * block_size as that.  None of these calls synchronizes or allocates. */
+typedef struct {
+  int32_t device;
+  int32_t batch;
+  int32_t n_kv_heads;
+  int32_t block_size;   /* tokens per block, any positive number */
+  int32_t max_blocks;   /* row stride of block_table */
+  int64_t n_blocks;
+  int32_t *block_table;
+} tq_pages;
+
+/* Grow every sequence by new_lens[b] tokens: take the blocks that this needs from a free list, write
+ * them into the block table, and give every (new token, KV head) its slot.
+ *   need_b = ceil((len_b + new_b) / block_size) - ceil(len_b / block_size) blocks, taken in the order
+ *   of the sequences from free_blocks[*free_head], free_blocks[*free_head + 1], ...
+ * A sequence is refused, with nothing of it changed, when it would pass max_blocks * block_size
+ * tokens, when its rows would pass n_slots, or when the free list, after what the sequences before it
+ * need (refused for its sake or not), has too few blocks left.  Its rows get slot -1, which
+ * tq_encode_kv and tq_append_kv skip.
+ *   seq_lens, new_lens  device int32 [batch]: tokens held, tokens to add
+ *   free_blocks         device int32 [n_free]; free_head device int32 [1]: entries already taken
+ *   seq_lens_out        device int32 [batch]: lengths after the call (may be seq_lens)
+ *   granted             device int32 [batch]: new_lens[b], or 0 where refused (may be new_lens)
+ *   free_head_out       device int32 [1] (may be free_head)
+ *   row_offsets         device int64 [batch + 1]: first row of each sequence, sum of new_lens behind it
+ *   new_slots           device int64 [n_slots]: row r's slots at r * n_kv_heads + h; -1 for the rows of
+ *                       refused sequences and behind the last sequence, so that a buffer of fixed size
+ *                       (a captured graph) serves every step
+ * Outputs overlap no other argument but where said.
+ * Errors: TQ_EINVAL (nulls, shapes, alignment, n_slots not a multiple of n_kv_heads), TQ_EUNSUPPORTED
+ * (sizes), TQ_ECUDA. */
+tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_lens, const int32_t *new_lens,
+                         const int32_t *free_blocks, int32_t n_free, const int32_t *free_head,
+                         int32_t *seq_lens_out, int32_t *granted, int32_t *free_head_out,
+                         int64_t *row_offsets, int64_t *new_slots, int64_t n_slots, void *stream);
+
+/* Append key and value rows to an uncompressed paged cache, and keep the smallest and largest value
+ * of every key channel per (block, KV head): the bounds that tq_block_scores reads.
+ * Sequence b's rows row_offsets[b] .. row_offsets[b] + granted[b] - 1 are its tokens
+ * seq_lens[b] - granted[b] .. seq_lens[b] - 1, as tq_page_extend leaves them.
+ *   seq_lens, granted, row_offsets  device, as written by tq_page_extend (lengths after the append)
+ *   k_new, v_new      device rows of dtype: head h of row r at r * ld + h * d elements (16-byte
+ *                     aligned, ld a multiple of 16 bytes, ld >= n_kv_heads * d)
+ *   n_rows            rows of k_new and v_new; sequences whose rows pass it are not appended
+ *   k_cache, v_cache  device [n_blocks][n_kv_heads][block_size][d] of dtype, or both NULL (bounds only:
+ *                     beside a compressed cache)
+ *   bounds            device [n_blocks][n_kv_heads][2][d] of dtype, lower then upper, or NULL.  A block
+ *                     that begins with a new token starts afresh; another one's bounds are widened.
+ * No block may hold new tokens of two sequences.
+ * d a multiple of 8 in [8, 256].
+ * Errors: TQ_EINVAL (nulls, shapes, alignment), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
+tq_status tq_append_kv(const tq_pages *pages, const int32_t *seq_lens, const int32_t *granted,
+                       const int64_t *row_offsets, const void *k_new, const void *v_new, tq_dtype dtype,
+                       int32_t d, int64_t n_rows, int64_t ld, void *k_cache, void *v_cache, void *bounds,
+                       void *stream);
+
+/* An upper bound of the inner products of every block's keys with the new token's queries:
+ *   scores[b * n_kv_heads + h][j] = max over the query heads hq of KV head h of
+ *                                   sum_c max(q_c lower_c, q_c upper_c)
+ * with the bounds of block block_table[b][j]; -infinity for j past the sequence's last block and for
+ * entries that name no block.
+ *   q       device [batch][n_q_heads][d] of dtype
+ *   bounds  device, as kept by tq_append_kv
+ *   scores  device fp32 [batch * n_kv_heads][max_blocks]
+ * d a multiple of 8 in [8, 256]; n_q_heads / n_kv_heads in [1, 16].
+ * Errors: TQ_EINVAL (nulls, shapes, alignment), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
+tq_status tq_block_scores(const tq_pages *pages, const int32_t *seq_lens, const void *q, tq_dtype dtype,
+                          int32_t n_q_heads, int32_t d, const void *bounds, float *scores, void *stream);
+
+/* Choose the blocks that each (sequence, KV head) reads: its first n_first and last n_last blocks and
+ * the best of the others by (score descending, index ascending), n_keep in all, or every block where it
+ * has no more than n_keep.  They come back in the order of the sequence as a block table of
+ * batch * n_kv_heads sequences with one KV head each:
+ *   sel_table[b * n_kv_heads + h][i] = block_table[b][j_i] * n_kv_heads + h  (-1 behind the last)
+ *   sel_lens [b * n_kv_heads + h]    = tokens in those blocks
+ * The same cache, read with n_kv_heads = 1 and n_blocks * n_kv_heads blocks, is then attended with
+ * tq_attend_paged or tq_attend_decode (max_blocks = n_keep, batch * n_kv_heads sequences).  The last
+ * block, the one that may be part full, is always the last of the row.
+ *   scores  device fp32 [batch * n_kv_heads][max_blocks]; NaN counts as -infinity
+ * n_first >= 0, n_last >= 1, n_first + n_last <= n_keep.  An entry of block_table that names no block
+ * comes back as -1 where it is chosen.
+ * Errors: TQ_EINVAL (nulls, shapes, counts, alignment), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
+tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_lens, const float *scores,
+                           int32_t n_keep, int32_t n_first, int32_t n_last, int32_t *sel_table,
+                           int32_t *sel_lens, void *stream);
+
+/* Attention of one new token per sequence over an uncompressed paged cache:
+ *   out[b][hq] = sum_t softmax_t(scale <q[b][hq], k_t>) v_t  over tokens t < seq_lens[b] of KV head
+ *   hq / (n_q_heads / n_kv_heads); zeros where no token is left.
+ *   max_seq_len  host-known upper bound of seq_lens (larger values are clamped to it), at most
+ *                max_blocks * block_size
+ *   q            device [batch][n_q_heads][d] of dtype
+ *   k_cache, v_cache  device [n_blocks][n_kv_heads][block_size][d] of dtype
+ *   scale        0 = 1/sqrt(d)
+ *   out          device [batch][n_q_heads][d] of out_dtype: TQ_F32, or dtype
+ *   ws           device workspace of tq_attend_paged_workspace_size() bytes, 16-byte aligned; its
+ *                contents do not matter, calls that overlap on the GPU need one each
+ * d a multiple of 8 in [8, 256]; n_q_heads / n_kv_heads in [1, 16].
+ * Errors: TQ_EINVAL (nulls, shapes, alignment, ws too small), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
+tq_status tq_attend_paged_workspace_size(const tq_pages *pages, int32_t max_seq_len, int32_t n_q_heads,
+                                         int32_t d, size_t *bytes);
+tq_status tq_attend_paged(const tq_pages *pages, const int32_t *seq_lens, int32_t max_seq_len,
+                          const void *q, const void *k_cache, const void *v_cache, tq_dtype dtype,
+                          int32_t n_q_heads, int32_t d, float scale, void *out, tq_dtype out_dtype,
+                          void *ws, size_t ws_bytes, void *stream);
 
 /* Instrumentation, off by default.  While enabled, every kernel that a data call launches is
  * bracketed by two CUDA events recorded on the caller's stream (so the pair times exactly that

@@ -13,7 +13,9 @@ namespace {
 
 const char *kNames[TQK_COUNT] = {"rotate_encode", "qjl_project", "rotate_query", "query_project", "scores",
                                  "attend_split", "attend_combine", "search_scan", "search_merge",
-                                 "attend_frag", "decode_prep", "encode_rows", "encode_qjl_tc"};
+                                 "attend_frag", "decode_prep", "encode_rows", "encode_qjl_tc",
+                                 "page_extend", "page_slots", "append_kv", "block_scores", "select_blocks",
+                                 "attend_paged", "attend_paged_merge"};
 
 struct Pending {
   int kind;

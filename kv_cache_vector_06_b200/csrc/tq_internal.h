@@ -81,11 +81,20 @@ class DeviceScope {
   int prev_ = -1;
 };
 
+// ---------------------------------------------------------------- paged caches (pages.cu)
+// Argument checks shared by the paged-cache calls; they also clear the thread's last error.
+tq_status tq_check_pages(const tq_pages *pages);
+tq_status tq_check_rows(tq_dtype dtype, int32_t d);            // row type and length
+tq_status tq_check_group(const tq_pages &pages, int32_t n_q_heads);  // query heads per KV head
+constexpr int kPagedMaxD = 256, kPagedMaxGroup = 16;
+static inline bool tq_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
 // ---------------------------------------------------------------- profile.cu
 enum TqKernelKind {
   TQK_ROTATE_ENCODE = 0, TQK_QJL_PROJECT, TQK_ROTATE_QUERY, TQK_QUERY_PROJECT, TQK_SCORES,
   TQK_ATTEND_SPLIT, TQK_ATTEND_COMBINE, TQK_SEARCH_SCAN, TQK_SEARCH_MERGE, TQK_ATTEND_FRAG, TQK_DECODE_PREP,
-  TQK_ENCODE_ROWS, TQK_ENCODE_QJL_TC, TQK_COUNT
+  TQK_ENCODE_ROWS, TQK_ENCODE_QJL_TC, TQK_PAGE_EXTEND, TQK_PAGE_SLOTS, TQK_APPEND_KV, TQK_BLOCK_SCORES,
+  TQK_SELECT_BLOCKS, TQK_ATTEND_PAGED, TQK_ATTEND_PAGED_MERGE, TQK_COUNT
 };
 bool tq_prof_on();  // per-kernel event profiling is enabled
 void tq_prof_begin(int kind, cudaStream_t st);

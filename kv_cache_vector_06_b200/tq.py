@@ -46,6 +46,11 @@ class AttnDesc(ctypes.Structure):
                 ("k", PackedC), ("v", PackedC), ("sparse_v", c_float)]
 
 
+class PagesC(ctypes.Structure):
+    _fields_ = [("device", c_int32), ("batch", c_int32), ("n_kv_heads", c_int32), ("block_size", c_int32),
+                ("max_blocks", c_int32), ("n_blocks", c_int64), ("block_table", c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m kv_cache_vector_06_b200.build`")
@@ -78,6 +83,17 @@ def _load():
         "tq_search_workspace_size": (st, [c_void_p, c_int32, c_int64, c_int32, POINTER(c_size_t)]),
         "tq_search_topk": (st, [c_void_p, c_void_p, c_int, c_int32, PackedC, c_int64, c_int32, c_void_p,
                                 c_void_p, c_void_p, c_size_t, c_void_p]),
+        "tq_page_extend": (st, [POINTER(PagesC), c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
+        "tq_append_kv": (st, [POINTER(PagesC), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int32, c_int64,
+                              c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "tq_block_scores": (st, [POINTER(PagesC), c_void_p, c_void_p, c_int, c_int32, c_int32, c_void_p, c_void_p,
+                                 c_void_p]),
+        "tq_select_blocks": (st, [POINTER(PagesC), c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                  c_void_p]),
+        "tq_attend_paged_workspace_size": (st, [POINTER(PagesC), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
+        "tq_attend_paged": (st, [POINTER(PagesC), c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int, c_int32, c_int32,
+                                 c_float, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
         "tq_profile_enable": (st, [c_int32]),
         "tq_profile_reset": (st, []),
         "tq_profile_read": (st, [c_int32, ctypes.c_char_p, c_int32, POINTER(c_int64), POINTER(c_double)]),
@@ -446,6 +462,162 @@ def search_topk(ctx: Context, q: torch.Tensor, db: Packed, k: int, n: int = None
                               _dev(out_scores, ctx.device, "out_scores", torch.float32),
                               _dev(out_idx, ctx.device, "out_idx", torch.int64), w, wb, _stream_ptr(stream)))
     return out_scores, out_idx
+
+
+class Pages:
+    """Paged-cache addressing (tq_pages): the block table [batch, max_blocks] and the cache's shape.
+    Holds the table's tensor; the calls below run on its device."""
+
+    def __init__(self, block_table: torch.Tensor, n_kv_heads: int, block_size: int, n_blocks: int):
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a tensor [batch, max_blocks]")
+        self.device = block_table.device.index
+        self.batch, self.max_blocks = block_table.shape
+        self.block_table = block_table
+        self.n_kv_heads, self.block_size, self.n_blocks = n_kv_heads, block_size, n_blocks
+        self._c = PagesC(self.device if block_table.is_cuda else -1, self.batch, n_kv_heads, block_size, self.max_blocks,
+                         n_blocks, _dev(block_table, self.device, "block_table", torch.int32))
+        self.ref = ctypes.byref(self._c)
+
+    def selected(self, sel_table: torch.Tensor) -> "Pages":
+        """The same cache as batch * n_kv_heads sequences of one KV head each, over the blocks that
+        select_blocks chose."""
+        return Pages(sel_table, 1, self.block_size, self.n_blocks * self.n_kv_heads)
+
+    def _lens(self, t, name: str, dtype=torch.int32, n: int = None):
+        if t.numel() != (self.batch if n is None else n):
+            raise ValueError(f"{name} must have {self.batch if n is None else n} entries")
+        return _dev(t, self.device, name, dtype)
+
+    def _rows(self, t, name: str, rows_per_block: int, d: int, dtype):
+        if t.shape[-1] != d or t.numel() != self.n_blocks * self.n_kv_heads * rows_per_block * d:
+            raise ValueError(f"{name} must be [{self.n_blocks}, {self.n_kv_heads}, {rows_per_block}, {d}]")
+        return _dev(t, self.device, name, dtype)
+
+    def _stream(self, stream):
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+
+def page_extend(pages: Pages, seq_lens, new_lens, free_blocks, free_head, n_rows: int = None, new_slots=None,
+                seq_lens_out=None, granted=None, free_head_out=None, row_offsets=None, stream=None):
+    """tq_page_extend: take blocks from free_blocks[free_head:] for new_lens more tokens per sequence,
+    write them into pages.block_table, and return (new_slots int64 [n_rows * n_kv_heads], seq_lens_out,
+    granted, free_head_out, row_offsets int64 [batch + 1]).  Outputs may be given; new_slots (or n_rows)
+    bounds the rows of one call."""
+    dev = free_head.device
+    if new_slots is None:
+        if n_rows is None:
+            raise ValueError("n_rows or new_slots is required")
+        new_slots = torch.empty(n_rows * pages.n_kv_heads, dtype=torch.int64, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(pages.batch, dtype=torch.int32, device=dev)
+    if granted is None:
+        granted = torch.empty(pages.batch, dtype=torch.int32, device=dev)
+    if free_head_out is None:
+        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+    if row_offsets is None:
+        row_offsets = torch.empty(pages.batch + 1, dtype=torch.int64, device=dev)
+    _check(LIB.tq_page_extend(
+        pages.ref, pages._lens(seq_lens, "seq_lens"), pages._lens(new_lens, "new_lens"),
+        _dev(free_blocks, pages.device, "free_blocks", torch.int32), free_blocks.numel(),
+        pages._lens(free_head, "free_head", n=1), pages._lens(seq_lens_out, "seq_lens_out"),
+        pages._lens(granted, "granted"), pages._lens(free_head_out, "free_head_out", n=1),
+        pages._lens(row_offsets, "row_offsets", torch.int64, pages.batch + 1),
+        _dev(new_slots, pages.device, "new_slots", torch.int64), new_slots.numel(), pages._stream(stream)))
+    return new_slots, seq_lens_out, granted, free_head_out, row_offsets
+
+
+def append_kv(pages: Pages, seq_lens, granted, row_offsets, k_new, v_new=None, k_cache=None, v_cache=None, bounds=None,
+              stream=None):
+    """tq_append_kv: write rows k_new, v_new ([n_rows, n_kv_heads, d], any row stride) into k_cache, v_cache
+    ([n_blocks, n_kv_heads, block_size, d]) and keep bounds ([n_blocks, n_kv_heads, 2, d]); lengths, granted
+    and row_offsets as page_extend returns them.  Without caches (None) only the bounds are kept."""
+    h = pages.n_kv_heads
+    rows = [k_new] if v_new is None else [k_new, v_new]
+    for t in rows:
+        if t.dim() != 3 or t.shape != k_new.shape or t.shape[1] != h or t.stride() != k_new.stride() or t.dtype != k_new.dtype:
+            raise ValueError(f"k_new and v_new must both be [n_rows, {h}, d] with one dtype and one row stride")
+    n, _, d = k_new.shape
+    if (d > 1 and k_new.stride(2) != 1) or (h > 1 and k_new.stride(1) != d):
+        raise ValueError("the heads of a row must lie side by side")
+    dt, dev = k_new.dtype, pages.device
+    ld = k_new.stride(0) if n > 1 else h * d
+    ptr = lambda t, name, per: None if t is None else pages._rows(t, name, per, d, dt)  # noqa: E731
+    _check(LIB.tq_append_kv(
+        pages.ref, pages._lens(seq_lens, "seq_lens"), pages._lens(granted, "granted"),
+        pages._lens(row_offsets, "row_offsets", torch.int64, pages.batch + 1),
+        _dev(k_new, dev, "k_new", contiguous=False), None if v_new is None else _dev(v_new, dev, "v_new", contiguous=False),
+        _dtype_code(k_new), d, n, ld, ptr(k_cache, "k_cache", pages.block_size), ptr(v_cache, "v_cache", pages.block_size),
+        ptr(bounds, "bounds", 2), pages._stream(stream)))
+
+
+def _queries(pages: Pages, q):
+    if q.dim() != 3 or q.shape[0] != pages.batch:
+        raise ValueError(f"q must be [{pages.batch}, n_q_heads, d]")
+    return _dev(q, pages.device, "q")
+
+
+def block_scores(pages: Pages, seq_lens, q, bounds, out=None, stream=None):
+    """tq_block_scores: upper bounds fp32 [batch * n_kv_heads, max_blocks] of the products of q
+    ([batch, n_q_heads, d]) with the keys of every block, from the bounds that append_kv keeps."""
+    rows = pages.batch * pages.n_kv_heads
+    qp = _queries(pages, q)
+    if out is None:
+        out = torch.empty(rows, pages.max_blocks, dtype=torch.float32, device=q.device)
+    if tuple(out.shape) != (rows, pages.max_blocks):
+        raise ValueError(f"out must be [{rows}, {pages.max_blocks}]")
+    _check(LIB.tq_block_scores(
+        pages.ref, pages._lens(seq_lens, "seq_lens"), qp, _dtype_code(q), q.shape[1], q.shape[2],
+        pages._rows(bounds, "bounds", 2, q.shape[2], q.dtype), _dev(out, pages.device, "out", torch.float32),
+        pages._stream(stream)))
+    return out
+
+
+def select_blocks(pages: Pages, seq_lens, scores, n_keep: int, n_first: int = 1, n_last: int = 1, table=None, lens=None,
+                  stream=None):
+    """tq_select_blocks: the first n_first, the last n_last and the best-scored other blocks of every
+    (sequence, KV head), n_keep in all, as a block table [batch * n_kv_heads, n_keep] and the tokens in it.
+    pages.selected(table) reads the same cache through it; for make_attn_desc it is the block_table of
+    batch * n_kv_heads sequences with n_kv_heads = 1."""
+    rows = pages.batch * pages.n_kv_heads
+    if tuple(scores.shape) != (rows, pages.max_blocks):
+        raise ValueError(f"scores must be [{rows}, {pages.max_blocks}]")
+    if table is None:
+        table = torch.empty(rows, max(n_keep, 0), dtype=torch.int32, device=scores.device)
+    if lens is None:
+        lens = torch.empty(rows, dtype=torch.int32, device=scores.device)
+    if tuple(table.shape) != (rows, max(n_keep, 0)):
+        raise ValueError(f"table must be [{rows}, {n_keep}]")
+    _check(LIB.tq_select_blocks(
+        pages.ref, pages._lens(seq_lens, "seq_lens"), _dev(scores, pages.device, "scores", torch.float32), n_keep, n_first,
+        n_last, _dev(table, pages.device, "table", torch.int32), pages._lens(lens, "lens", n=rows), pages._stream(stream)))
+    return table, lens
+
+
+def attend_paged_workspace_size(pages: Pages, max_seq_len: int, n_q_heads: int, d: int) -> int:
+    b = c_size_t()
+    _check(LIB.tq_attend_paged_workspace_size(pages.ref, max_seq_len, n_q_heads, d, ctypes.byref(b)))
+    return b.value
+
+
+def attend_paged(pages: Pages, seq_lens, max_seq_len: int, q, k_cache, v_cache, scale: float = 0.0, out=None, ws=None,
+                 stream=None):
+    """tq_attend_paged: attention of one new token per sequence, q [batch, n_q_heads, d], over the
+    uncompressed caches [n_blocks, n_kv_heads, block_size, d] of q's dtype.  out: fp32 (the default) or
+    q's dtype."""
+    qp = _queries(pages, q)
+    _, hq, d = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    w, wb = _workspace(attend_paged_workspace_size(pages, max_seq_len, hq, d), pages.device, ws)
+    _check(LIB.tq_attend_paged(
+        pages.ref, pages._lens(seq_lens, "seq_lens"), max_seq_len, qp,
+        pages._rows(k_cache, "k_cache", pages.block_size, d, q.dtype),
+        pages._rows(v_cache, "v_cache", pages.block_size, d, q.dtype), _dtype_code(q), hq, d, scale,
+        _dev(out, pages.device, "out"), _dtype_code(out), w, wb, pages._stream(stream)))
+    return out
 
 
 def profile_enable(on: bool = True):

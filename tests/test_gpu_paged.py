@@ -1,0 +1,526 @@
+"""The paged-cache calls (tq_page_extend, tq_append_kv, tq_block_scores, tq_select_blocks,
+tq_attend_paged) against the fp64 oracle, each alone and run together as a serving step.
+
+Whole numbers and copies are equal.  Tolerances of the others count roundings of 32-bit arithmetic:
+  products   bf16 x bf16 is exact in fp32; an fp32 product, also one made of TF32 parts of the operands
+             (each part rounded to 2^-11 of its value, the product of the two tails dropped), is within
+             3 x 2^-22 of |x y|
+  sums       n terms in any order: at most n roundings of 2^-23 (a tensor core's sum may truncate) of the
+             sum of the absolute terms
+  softmax    a logit that is off by e moves its weight by a factor e^(+-e); exp itself is within 2^-21; the
+             weights, the value products and the sums then round like the above
+  output     half a step of the output's type"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import attention as oattn
+from oracle import paged
+from parity import Quantizer, assert_attention_close, oracle_heads
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from kv_cache_vector_06_b200 import tq as _tq
+    return _tq
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def rows(*shape, seed, dtype):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def tables(lens, width, block, seed, spare=3):
+    """A block table with the blocks of `lens` in one random order (-1 behind them) and the number of blocks."""
+    rng = np.random.default_rng(seed)
+    held = [-(-n // block) for n in lens]
+    n_blocks = sum(held) + spare
+    perm = rng.permutation(n_blocks)
+    t = np.full((len(lens), width), -1)
+    at = 0
+    for b, k in enumerate(held):
+        t[b, :k] = perm[at:at + k]
+        at += k
+    return t, n_blocks
+
+
+# ------------------------------------------------------------------------------------ page_extend
+def check_extend(tq, table, lens, new, free, head, n_rows, n_kv, block, n_blocks, in_place):
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    l, g, hd = i32(lens), i32(new), i32([head])
+    outs = dict(seq_lens_out=l, granted=g, free_head_out=hd) if in_place else {}
+    slots, after, granted, head2, off = tq.page_extend(pages, l, g, i32(free), hd, n_rows=n_rows, **outs)
+    ref = paged.extend(table, lens, new, free, head, n_rows, n_kv, block, n_blocks)
+    got = [x.cpu().numpy() for x in (pages.block_table, after, granted, head2, off, slots)]
+    for name, x, y in zip(("table", "lens", "granted", "head", "offsets", "slots"), got, ref):
+        assert np.array_equal(x.reshape(-1), np.asarray(y).reshape(-1)), name
+
+
+@pytest.mark.parametrize("batch,n_kv,block,lo,hi,most", [(1, 1, 1, 0, 0, 1), (1, 8, 16, 40, 40, 1), (7, 3, 24, 0, 90, 50),
+                                                        (64, 8, 16, 0, 300, 1), (33, 2, 128, 0, 700, 400),
+                                                        (2500, 1, 16, 0, 60, 9), (3, 5, 7, 100, 3000, 20000)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_extend(tq, batch, n_kv, block, lo, hi, most, in_place):
+    rng = np.random.default_rng(batch + block)
+    lens, new = rng.integers(lo, hi + 1, batch), rng.integers(0, most + 1, batch)
+    width = -(-(hi + most) // block)
+    table, used = tables(lens, width, block, seed=1)
+    need = int(sum(-(-(n + m) // block) - -(-n // block) for n, m in zip(lens, new)))
+    free = rng.permutation(used + need + 4)
+    for short, pad in ((0, 11), (max(1, need // 3), 0), (-2, -(int(new.sum()) // 2))):
+        # enough blocks; too few of them; too few rows
+        n_free = max(2, 2 + need - short)
+        check_extend(tq, table, lens, new, free[:n_free], 2, int(new.sum()) + pad, n_kv, block, used + need + 4, in_place)
+
+
+def test_extend_odd_values(tq):
+    """Negative lengths, a length past the table, nothing to add, no rows at all, free entries and table
+    entries that name no block, a head past the list, sums past 32 bits."""
+    table = np.array([[0, 1, 2], [3, -1, 9], [4, 99, 5], [-7, -1, -1], [6, 7, 8]])
+    for lens, new, free, head in (([-3, 5, 9, 2, 0], [4, 0, 2, 1, -5], [50, 11, 12], 0), ([12, 13, 2, 0, 1], [1, 1, 3, 12, 12], [10, -1, 11, 12, 13, 14], 1),
+                                  ([1, 1, 1, 1, 1], [9, 9, 9, 9, 9], [10, 11], 7), ([1, 1, 1, 1, 1], [2**31 - 1] * 5, [10], 0)):
+        for n_rows in (0, 1, 30):
+            lens0 = [max(x, 0) for x in lens]
+            if n_rows and head <= len(free):
+                check_extend(tq, table, lens0, new, free, head, n_rows, 2, 4, 20, False)
+            pages = tq.Pages(i32(table), 2, 4, 20)
+            slots, after, granted, head2, off = tq.page_extend(pages, i32(lens), i32(new), i32(free), i32([head]), n_rows=n_rows)
+            ref = paged.extend(table, lens, new, free, min(head, len(free)), n_rows, 2, 4, 20)
+            assert np.array_equal(slots.cpu().numpy(), ref[5]) and np.array_equal(off.cpu().numpy(), ref[4])
+            assert after.tolist() == ref[1].tolist() and granted.tolist() == ref[2].tolist() and head2.item() == ref[3]
+    pages = tq.Pages(torch.zeros(0, 4, dtype=torch.int32, device="cuda"), 2, 4, 20)
+    none = i32([])
+    slots, _, _, head, off = tq.page_extend(pages, none, none, i32([1, 2]), i32([1]), n_rows=3)
+    assert slots.tolist() == [-1] * 6 and head.item() == 1 and off.tolist() == [0]
+
+
+# ------------------------------------------------------------------------------------ append_kv
+def append_case(tq, lens, granted, n_kv, block, d, dtype, seed, gap=0, offsets=None, table=None, caches=True, with_bounds=True,
+                n_rows=None):
+    """lens: after the append."""
+    width = max(1, max(-(-n // block) for n in lens) + 1)
+    if table is None:
+        table, n_blocks = tables(lens, width, block, seed)
+    else:
+        n_blocks = int(np.max(table)) + 1
+    off = np.concatenate([[0], np.cumsum(granted)]) if offsets is None else np.asarray(offsets)
+    n = int(off[-1]) if n_rows is None else n_rows
+    kv = rows(n, 2, n_kv * d + gap, seed=seed, dtype=dtype).cuda()
+    k, v = (kv[:, i, :n_kv * d].unflatten(1, (n_kv, d)) for i in (0, 1))
+    kc, vc = (torch.full((n_blocks, n_kv, block, d), math.nan, dtype=dtype).cuda() for _ in (0, 1))
+    bd = rows(n_blocks, n_kv, 2, d, seed=seed + 1, dtype=dtype).sort(2).values.cuda()
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    before = [x.double().cpu().numpy() for x in (kc, vc, bd)]
+    tq.append_kv(pages, i32(lens), i32(granted), torch.as_tensor(off).cuda(), k, v if caches else None,
+                 kc if caches else None, vc if caches else None, bd if with_bounds else None)
+    grown = [g if off[b] + g <= n else 0 for b, g in enumerate(granted)]
+    ref = paged.append(table, lens, grown, off, k.double().cpu().numpy(), v.double().cpu().numpy(), *before, block)
+    for name, x, y, z, on in zip(("k_cache", "v_cache", "bounds"), (kc, vc, bd), ref, before, (caches, caches, with_bounds)):
+        np.testing.assert_array_equal(x.double().cpu().numpy(), y if on else z, err_msg=name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,n_kv,block", [(128, 8, 16), (64, 1, 16), (80, 3, 24), (256, 2, 128), (8, 5, 1), (192, 2, 7), (96, 16, 64)])
+def test_append(tq, dtype, d, n_kv, block):
+    append_case(tq, [1, 16, 17, 100, 33, 700, 5], [1, 16, 1, 99, 0, 650, 5], n_kv, block, d, dtype, seed=d + block, gap=24)
+
+
+@pytest.mark.parametrize("granted", [[1], [0], [4]])
+def test_append_one_sequence(tq, granted):
+    append_case(tq, [37], granted, 2, 16, 128, BF16, seed=3, n_rows=4)
+
+
+def test_append_refused_rows_and_bounds_only(tq):
+    """Refused sequences keep their rows unread (offsets count them); a sequence whose rows pass n_rows is
+    not appended; caches and bounds each without the other; table entries that name no block."""
+    lens, granted, off = [20, 7, 40, 9], [20, 0, 3, 9], [0, 20, 31, 34, 43]
+    for kw in (dict(), dict(caches=False), dict(with_bounds=False), dict(n_rows=40)):
+        append_case(tq, lens, granted, 2, 16, 64, BF16, seed=5, offsets=off, **kw)
+    table = np.array([[3, -1, 4], [0, 0, 0], [1, 2, 70000], [-5, 6, 6]])
+    table[2, 2] = -9
+    append_case(tq, [40, 0, 48, 30], [33, 0, 48, 20], 2, 16, 64, F32, seed=6, table=table)
+
+
+# ------------------------------------------------------------------------------------ block_scores
+def check_scores(tq, lens, n_kv, group, block, d, dtype, seed, width=None, table=None):
+    if table is None:
+        table, n_blocks = tables([max(n, 0) for n in lens], width or max(1, max(-(-n // block) for n in lens)), block, seed)
+    else:
+        n_blocks = 7
+    bd = (rows(n_blocks, n_kv, 2, d, seed=seed, dtype=dtype) * torch.exp(rows(n_kv, 1, d, seed=seed + 1, dtype=dtype))).sort(2).values.cuda()
+    q = rows(len(lens), n_kv * group, d, seed=seed + 2, dtype=dtype).cuda()
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    got = tq.block_scores(pages, i32(lens), q, bd).double().cpu().numpy()
+    b64, q64 = bd.double().cpu().numpy(), q.double().cpu().numpy()
+    ref = paged.block_scores(table, lens, q64, b64, block)
+    assert np.array_equal(np.isfinite(got), np.isfinite(ref)) and np.all(got[~np.isfinite(ref)] == -np.inf)
+    # sum of the absolute terms of the largest query head bounds every head's rounding
+    big = paged.block_scores(table, lens, np.abs(q64), np.repeat(np.abs(b64).max(2, keepdims=True), 2, axis=2), block)
+    fin = np.isfinite(ref)
+    tol = (2 * d * 2.0 ** -23 + 3 * 2.0 ** -22) * big[fin]
+    assert np.all(np.abs(got[fin] - ref[fin]) <= tol), np.max(np.abs(got[fin] - ref[fin]) / tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,n_kv,group,block", [(128, 8, 4, 16), (64, 1, 1, 16), (80, 3, 5, 24), (256, 2, 8, 128), (8, 2, 16, 1),
+                                                (192, 2, 7, 32), (96, 4, 2, 64), (128, 1, 16, 8), (256, 1, 9, 16), (128, 2, 8, 16)])
+def test_scores(tq, dtype, d, n_kv, group, block):
+    check_scores(tq, [1, 0, 16, 17, 1000, 333, 2049, 5], n_kv, group, block, d, dtype, seed=d + group)
+
+
+def test_scores_odd_tables(tq):
+    """Entries that name no block, a table wider than the sequences, a length past the table, a negative one."""
+    t = np.array([[0, -1, 5, 3, 7], [6, 100, -4, 2, 1], [1, 2, 3, 4, 5], [5, 5, 5, 5, 5]])
+    check_scores(tq, [80, 65, -4, 200], 2, 4, 16, 128, BF16, seed=9, table=t)
+    check_scores(tq, [80, 65, -4, 200], 2, 4, 16, 64, F32, seed=9, table=t)
+    check_scores(tq, [3, 30], 2, 4, 16, 128, BF16, seed=10, width=70)
+
+
+def test_scores_bound_the_keys(tq):
+    """Scores from appended bounds are not below any key's product (the sums' rounding apart)."""
+    n, n_kv, group, d, block = 1000, 2, 4, 128, 16
+    table, n_blocks = tables([n], 63, block, 4)
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    k = rows(n, n_kv, d, seed=1, dtype=BF16).cuda()
+    bd = torch.empty(n_blocks, n_kv, 2, d, dtype=BF16).cuda()
+    tq.append_kv(pages, i32([n]), i32([n]), torch.tensor([0, n]).cuda(), k, bounds=bd)
+    q = rows(1, n_kv * group, d, seed=2, dtype=BF16).cuda()
+    s = tq.block_scores(pages, i32([n]), q, bd).double().cpu()
+    prod = torch.einsum("hgd,nhd->hgn", q.double().cpu().view(n_kv, group, d), k.double().cpu()).amax(1)
+    best = torch.nn.functional.pad(prod, (0, 63 * 16 - n), value=-math.inf).view(n_kv, 63, 16).amax(2)
+    assert torch.all(best <= s + 1e-3) and torch.all(s < best + 200)
+
+
+# ------------------------------------------------------------------------------------ select_blocks
+def check_select(tq, lens, scores, n_kv, block, keep, first, last, seed=0, table=None):
+    width = scores.shape[1]
+    if table is None:
+        table, n_blocks = tables([min(max(n, 0), width * block) for n in lens], width, block, seed)
+    else:
+        n_blocks = 9
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    t, n = tq.select_blocks(pages, i32(lens), torch.as_tensor(scores, dtype=F32).cuda(), keep, n_first=first, n_last=last)
+    rt, rn = paged.select(table, lens, scores.astype(np.float32).astype(np.float64), n_kv, block, n_blocks, keep, first, last)
+    assert np.array_equal(t.cpu().numpy(), rt) and np.array_equal(n.cpu().numpy(), rn)
+
+
+@pytest.mark.parametrize("n_kv,block,width,keep,first,last", [(1, 16, 1, 1, 0, 1), (2, 16, 40, 8, 1, 2), (3, 24, 600, 64, 4, 8),
+                                                             (2, 1, 5000, 1000, 0, 1), (1, 64, 33, 33, 1, 1), (1, 16, 100, 300, 2, 3),
+                                                             (2, 16, 9000, 3, 1, 2), (1, 8, 70000, 257, 1, 4), (1, 8, 513, 512, 0, 512)])
+def test_select(tq, n_kv, block, width, keep, first, last):
+    rng = np.random.default_rng(width + keep)
+    lens = [width * block, 0, 1, width * block - 1, (width * block + 1) // 2, min(width, keep) * block, min(width, keep + 1) * block]
+    for kind in range(3):
+        s = rng.standard_normal((len(lens) * n_kv, width))
+        if kind == 1:
+            s = np.round(s * 2)  # many ties, -0 and +0 among them
+        if kind == 2:
+            s = s * 1e-30 * (rng.random(s.shape) < 0.5) - (rng.random(s.shape) < 0.3) * 1e30
+        check_select(tq, lens, s, n_kv, block, keep, first, last)
+
+
+def test_select_odd_scores(tq):
+    """All equal; infinities and NaN; scores behind the last block are not read as candidates; lengths past
+    the table; entries that name no block."""
+    inf, nan = math.inf, math.nan
+    lens = [160, 1000, -2, 75]
+    s = np.zeros((4, 10))
+    check_select(tq, lens, s, 1, 16, 4, 1, 1)
+    s[0] = [inf, nan, -inf, inf, 0.0, -0.0, nan, 3, -inf, 1]
+    s[1] = nan
+    s[3] = [1, 2, 3, 4, 5, inf, nan, inf, nan, inf]
+    for keep in (2, 3, 4, 5, 9):
+        check_select(tq, lens, s, 1, 16, keep, 1, 1)
+    t = np.array([[0, 1, -1, 3, 50, 5, 6, 7, 8, 2]] * 4)
+    check_select(tq, lens, s, 1, 16, 6, 0, 1, table=t)
+
+
+# ------------------------------------------------------------------------------------ attend_paged
+def attend_tolerance(table, lens, q, kc, vc, block, scale, dtype, out_dtype):
+    """Bound on |out - reference| [batch, n_q, d] by the counts of this file's docstring."""
+    n_kv, d = kc.shape[1], q.shape[2]
+    group = q.shape[1] // n_kv
+    tol = np.zeros(q.shape)
+    for b in range(len(lens)):
+        t = np.arange(max(int(lens[b]), 0))
+        e = np.asarray(table[b], dtype=np.int64)[t // block]
+        ok = (e >= 0) & (e < kc.shape[0])
+        t, e = t[ok] % block, e[ok]
+        for hq in range(q.shape[1]) if len(t) else ():
+            k, v = kc[e, hq // group, t], vc[e, hq // group, t]
+            s = scale * (k @ q[b, hq])
+            mag = abs(scale) * (np.abs(k) @ np.abs(q[b, hq]))  # the absolute terms, whatever the sign of scale
+            off = np.max(mag) * (d * 2.0 ** -23 + 3 * 2.0 ** -22) + 2 * np.max(np.abs(s)) * 2.0 ** -23 + 2.0 ** -20
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            av = w @ np.abs(v)
+            o = np.abs(w @ v)
+            tol[b, hq] = (2 * off + (2 * len(t) + 8) * 2.0 ** -23 + 6 * 2.0 ** -22) * av
+            tol[b, hq] += torch.finfo(out_dtype).eps / 2 * (o + tol[b, hq])
+    return tol
+
+
+def check_attend(tq, lens, n_kv, group, block, d, dtype, out_dtype=F32, seed=0, scale=0.0, table=None, max_len=None, poison=True,
+                 key_scale=1.0, ws=None):
+    width = max(1, max(-(-max(n, 0) // block) for n in lens))
+    if table is None:
+        table, n_blocks = tables([max(n, 0) for n in lens], width, block, seed)
+    else:
+        n_blocks = 9
+        width = np.shape(table)[1]
+    kc, vc = (rows(n_blocks, n_kv, block, d, seed=seed + i, dtype=dtype) for i in (1, 2))
+    kc = (kc * key_scale).to(dtype)
+    ref_k, ref_v = kc.double().numpy(), vc.double().numpy()
+    if poison:
+        # whatever lies outside the sequences must not be looked at
+        held = torch.zeros(n_blocks, block, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for t in range(min(max(n, 0), width * block if max_len is None else max_len)):
+                if 0 <= table[b][t // block] < n_blocks:
+                    held[table[b][t // block], t % block] = True
+        bad = (~held)[:, None, :, None].expand_as(kc)
+        kc, vc = kc.masked_fill(bad, math.nan), vc.masked_fill(bad, math.inf)
+    q = rows(len(lens), n_kv * group, d, seed=seed + 3, dtype=dtype)
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    max_len = width * block if max_len is None else max_len
+    out = torch.full(q.shape, math.nan, dtype=out_dtype).cuda()
+    got = tq.attend_paged(pages, i32(lens), max_len, q.cuda(), kc.cuda(), vc.cuda(), scale=scale, out=out, ws=ws)
+    got = got.double().cpu().numpy()
+    n = [min(max(x, 0), max_len) for x in lens]
+    q64 = q.double().numpy()
+    ref = paged.attend(table, n, q64, ref_k, ref_v, block, scale)
+    tol = attend_tolerance(table, n, q64, ref_k, ref_v, block, scale or d ** -0.5, dtype, out_dtype)
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), f"{np.max(err[tol > 0] / tol[tol > 0])} of the tolerance, zeros {np.max(err[tol == 0], initial=0)}"
+    assert np.all(got[[x == 0 for x in n]] == 0)
+    return got
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,n_kv,group,block", [(128, 8, 4, 16), (64, 1, 1, 16), (80, 3, 5, 24), (256, 2, 8, 128), (8, 2, 16, 1),
+                                                (192, 2, 7, 32), (96, 4, 2, 64), (128, 1, 16, 8), (256, 1, 9, 16), (128, 2, 8, 16),
+                                                (64, 2, 12, 5), (16, 1, 3, 16), (120, 2, 6, 16)])
+def test_attend(tq, dtype, d, n_kv, group, block):
+    check_attend(tq, [1, 0, 16, 17, 1000, 333, 2049, 5], n_kv, group, block, d, dtype, seed=d + group)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens", [[1], [0], [15], [16], [9001], [40000], [0, 0, 0], [4096] * 3, [20000, 1, 1, 1, 1, 1, 1, 1]])
+def test_attend_lengths(tq, dtype, lens):
+    check_attend(tq, lens, 2, 4, 16, 128, dtype, seed=len(lens) + lens[0])
+
+
+def test_attend_many_sequences(tq):
+    """More rows than the GPU has room for at once, ragged."""
+    rng = np.random.default_rng(0)
+    check_attend(tq, rng.integers(0, 200, 301).tolist(), 3, 2, 16, 64, BF16, seed=8)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_bf16_output(tq, d):
+    check_attend(tq, [700, 0, 31, 3000], 2, 4, 16, d, BF16, out_dtype=BF16, seed=11)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_scales_and_sharp_softmax(tq, dtype):
+    """A given scale, a negative one, and logits so far apart that one token holds the weight."""
+    for scale, key_scale in ((1.0, 1.0), (-0.25, 1.0), (0.0, 16.0)):
+        check_attend(tq, [500, 3, 1500], 2, 4, 16, 128, dtype, seed=12, scale=scale, key_scale=key_scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_odd_tables(tq, dtype):
+    """Entries that name no block leave their tokens out (a row of nothing else gives zeros), blocks shared by
+    two sequences, lengths past max_seq_len and negative ones."""
+    t = np.array([[0, -1, 5, 3], [100, -4, 9, 1 << 30], [5, 2, 3, 4], [1, 2, -1, -1]])
+    check_attend(tq, [64, 64, 50, 40], 2, 4, 16, 128, dtype, seed=13, table=t)
+    check_attend(tq, [1000, -5, 33, 30], 2, 4, 16, 64, dtype, seed=14, table=t, max_len=33)
+
+
+def test_attend_workspace_reused(tq):
+    """One workspace, filled with NaN, for calls of different shapes in a row."""
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8).cuda()
+    for seed, lens in enumerate(([3000, 20, 700], [40], [9000], [1, 0, 2], [3000, 20, 700])):
+        check_attend(tq, lens, 2, 4, 16, 128, BF16, seed=20 + seed, ws=ws)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_far_offsets(tq, dtype):
+    """A cache whose element offsets pass 2^32: append to its last blocks, then score and attend there."""
+    d, n_kv, block = 128, 4, 16
+    n_blocks = (1 << 32) // (d * n_kv * block) + 500
+    kc, vc = (torch.empty(n_blocks, n_kv, block, d, dtype=dtype, device="cuda") for _ in (0, 1))
+    bd = torch.empty(n_blocks, n_kv, 2, d, dtype=dtype, device="cuda")
+    n, group = 900, 2
+    rng = np.random.default_rng(1)
+    held = -(-n // block)
+    table = np.stack([n_blocks - 1 - rng.permutation(400)[:held], rng.permutation(400)[:held]])
+    k, v = (rows(2 * n, n_kv, d, seed=s, dtype=dtype) for s in (1, 2))
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    lens = i32([n, n])
+    tq.append_kv(pages, lens, lens, torch.tensor([0, n, 2 * n]).cuda(), k.cuda(), v.cuda(), kc, vc, bd)
+    q = rows(2, n_kv * group, d, seed=3, dtype=dtype)
+    got = tq.attend_paged(pages, lens, n, q.cuda(), kc, vc).double().cpu().numpy()
+    small = np.stack([np.arange(held), np.arange(held) + held])  # the same tokens in a small cache
+    kc2, vc2 = (np.pad(x.double().numpy().reshape(2, n, n_kv, d), ((0, 0), (0, held * block - n), (0, 0), (0, 0)))
+                .reshape(2 * held, block, n_kv, d).transpose(0, 2, 1, 3) for x in (k, v))
+    q64 = q.double().numpy()
+    ref = paged.attend(small, [n, n], q64, kc2, vc2, block)
+    assert np.all(np.abs(got - ref) <= attend_tolerance(small, [n, n], q64, kc2, vc2, block, d ** -0.5, dtype, F32))
+    s = tq.block_scores(pages, lens, q.cuda(), bd).cpu().double().numpy()
+    pad = np.concatenate([k.double().numpy().reshape(2, n, n_kv, d), np.repeat(k.double().numpy().reshape(2, n, n_kv, d)[:, -1:], held * block - n, axis=1)], 1)
+    x = pad.reshape(2 * held, block, n_kv, d)
+    bounds = np.stack([x.min(1), x.max(1)], axis=2)
+    np.testing.assert_allclose(s, paged.block_scores(small, [n, n], q64, bounds, block), rtol=1e-4)
+
+
+# ------------------------------------------------------------------------------------ together
+def serve(tq, steps, graph, stream=None, seed=0):
+    """Admit four sequences, then `steps` decode steps: grow, append, score, choose, attend, all on the GPU.  Returns
+    what every step attended and the state."""
+    n_kv, group, d, block, width, keep = 2, 4, 128, 16, 24, 9
+    dev = torch.device("cuda")
+    pages = tq.Pages(torch.full((4, width), -1, dtype=torch.int32, device=dev), n_kv, block, 64)
+    free = torch.randperm(64, generator=torch.Generator().manual_seed(seed)).to(torch.int32).cuda()
+    head, lens = torch.zeros(1, dtype=torch.int32, device=dev), torch.zeros(4, dtype=torch.int32, device=dev)
+    kc, vc = (torch.zeros(64, n_kv, block, d, dtype=BF16, device=dev) for _ in (0, 1))
+    bd = torch.zeros(64, n_kv, 2, d, dtype=BF16, device=dev)
+    new = i32([301, 0, 16, 100])
+    k, v = (rows(417, n_kv, d, seed=seed + i, dtype=BF16).cuda() for i in (1, 2))
+    _, _, granted, _, off = tq.page_extend(pages, lens, new, free, head, n_rows=417, seq_lens_out=lens, free_head_out=head)
+    tq.append_kv(pages, lens, granted, off, k, v, kc, vc, bd)
+    ks, vs = (rows(steps, 4, n_kv, d, seed=seed + i, dtype=BF16).cuda() for i in (3, 4))
+    qs = rows(steps, 4, n_kv * group, d, seed=seed + 5, dtype=BF16).cuda()
+    one, knew, vnew, q = i32([1, 1, 1, 1]), ks[0].clone(), vs[0].clone(), qs[0].clone()
+    keep_all = {}
+
+    def step():
+        slots, _, granted, _, off = tq.page_extend(pages, lens, one, free, head, n_rows=4, seq_lens_out=lens, free_head_out=head)
+        tq.append_kv(pages, lens, granted, off, knew, vnew, kc, vc, bd)
+        s = tq.block_scores(pages, lens, q, bd)
+        table, held = tq.select_blocks(pages, lens, s, keep, n_first=1, n_last=2)
+        sub = pages.selected(table)
+        full = tq.attend_paged(pages, lens, width * block, q, kc, vc)
+        part = tq.attend_paged(sub, held, keep * block, q.view(4 * n_kv, group, d), kc, vc)
+        keep_all["out"] = (slots, s, table, held, full, part)
+
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        saved = [x.clone() for x in (pages.block_table, lens, head, kc, vc, bd)]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        with torch.cuda.graph(g):
+            step()
+        for x, y in zip((pages.block_table, lens, head, kc, vc, bd), saved):
+            x.copy_(y)
+    outs = []
+    for i in range(steps):
+        knew.copy_(ks[i]), vnew.copy_(vs[i]), q.copy_(qs[i])
+        g.replay() if graph else step()
+        outs.append([x.clone() for x in keep_all["out"]])
+    torch.cuda.synchronize()
+    return outs, dict(pages=pages, lens=lens, kc=kc, vc=vc, bd=bd, qs=qs, free=free, group=group, keep=keep, block=block)
+
+
+def test_serving_steps(tq):
+    """Prompts, then 20 decode steps (sequences cross block borders, one starts empty): every step's choice and
+    both attentions follow the oracle on the cache as it is; the eager and the captured run give the same bits."""
+    outs, s = serve(tq, 20, graph=False)
+    assert s["lens"].tolist() == [321, 20, 36, 120]
+    kc, vc = s["kc"].double().cpu().numpy(), s["vc"].double().cpu().numpy()
+    bd, table = s["bd"].double().cpu().numpy(), s["pages"].block_table.cpu().numpy()
+    lens, q64 = s["lens"].cpu().numpy(), s["qs"][-1].double().cpu().numpy()
+    _, sc, sel, held, full, part = (x.cpu().numpy() for x in outs[-1])
+    ref_bd = np.zeros_like(bd)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // 16)):
+            x = kc[table[b, j], :, :min(16, n - 16 * j)]
+            ref_bd[table[b, j], :, 0], ref_bd[table[b, j], :, 1] = x.min(1), x.max(1)
+    used = np.unique(table[table >= 0])
+    assert np.array_equal(bd[used], ref_bd[used])
+    ref_sel, ref_held = paged.select(table, lens, sc.astype(np.float64), 2, 16, 64, s["keep"], 1, 2)
+    assert np.array_equal(sel, ref_sel) and np.array_equal(held, ref_held)
+    assert np.all(np.abs(full - paged.attend(table, lens, q64, kc, vc, 16)) <=
+                  attend_tolerance(table, lens, q64, kc, vc, 16, 128 ** -0.5, BF16, F32))
+    k1, v1, q1 = kc.reshape(128, 1, 16, 128), vc.reshape(128, 1, 16, 128), q64.reshape(8, 4, 128)
+    assert np.all(np.abs(part - paged.attend(sel, held, q1, k1, v1, 16)) <=
+                  attend_tolerance(sel, held, q1, k1, v1, 16, 128 ** -0.5, BF16, F32))
+    again, _ = serve(tq, 20, graph=True)
+    for x, y in zip(outs, again):
+        for u, w in zip(x, y):
+            assert torch.equal(u, w)
+
+
+def test_serving_steps_on_two_streams(tq):
+    """Two independent runs queued on two streams at once give what each gives alone."""
+    alone = [serve(tq, 6, graph=False, seed=s)[0] for s in (0, 50)]
+    streams = [torch.cuda.Stream() for _ in (0, 1)]
+    torch.cuda.synchronize()
+    both = []
+    for s, st in zip((0, 50), streams):
+        with torch.cuda.stream(st):
+            both.append(serve(tq, 6, graph=False, seed=s)[0])
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        for u, w in zip(x, y):
+            assert all(torch.equal(a, b) for a, b in zip(u, w))
+
+
+@pytest.mark.parametrize("vlayout", [0, 1])
+def test_compressed_cache_through_pages(tq, vlayout):
+    """page_extend's slots encode the compressed cache, its new_slots serve tq_decode_step, and the chosen blocks
+    are attended with tq_attend_decode as one-head sequences (general and tensor-core attention)."""
+    n_kv, group, d, block, width, keep = 2, 4, 128, 16, 40, 6
+    new = [301, 16, 600, 33]
+    kq, vq = Quantizer(d, 2, d, seed=60), Quantizer(d, 3, 0, seed=61, layout=vlayout)
+    cap = 90
+    kp, vp = tq.Packed.allocate(kq.ctx, cap * n_kv * block), tq.Packed.allocate(vq.ctx, cap * n_kv * block)
+    pages = tq.Pages(torch.full((4, width), -1, dtype=torch.int32, device="cuda"), n_kv, block, cap)
+    free = torch.randperm(cap, generator=torch.Generator().manual_seed(5)).to(torch.int32).cuda()
+    head, lens = i32([0]), i32([0, 0, 0, 0])
+    n = sum(new) + 7  # a padded batch: the rows behind the last sequence are not stored
+    k, v = (rows(n, n_kv, d, seed=s, dtype=BF16).cuda() for s in (62, 63))
+    slots, lens, granted, head, off = tq.page_extend(pages, lens, i32(new), free, head, n_rows=n)
+    tq.encode_kv(kq.ctx, k.view(-1, d), kp, slots=slots)
+    tq.encode_kv(vq.ctx, v.view(-1, d), vp, slots=slots)
+    bd = torch.empty(cap, n_kv, 2, d, dtype=BF16, device="cuda")
+    tq.append_kv(pages, lens, granted, off, k, bounds=bd)
+    # one decode step of the compressed path with the slots of the grown sequences
+    k1, v1 = (rows(4, n_kv, d, seed=s, dtype=BF16).cuda() for s in (64, 65))
+    q = rows(4, n_kv * group, d, seed=66, dtype=BF16).cuda()
+    slots, lens, granted, head, off = tq.page_extend(pages, lens, i32([1] * 4), free, head, n_rows=4)
+    desc = tq.make_attn_desc(kq.ctx, vq.ctx, q.shape, kp, vp, lens, width * block, block_table=pages.block_table,
+                             block_size=block, n_kv_heads=n_kv)
+    out = tq.decode_step(kq.ctx, vq.ctx, q, k1.view(-1, d), v1.view(-1, d), slots, desc)
+    tq.append_kv(pages, lens, granted, off, k1, bounds=bd)
+    s = tq.block_scores(pages, lens, q, bd)
+    table, held = tq.select_blocks(pages, lens, s, keep, n_first=1, n_last=2)
+    part = tq.attend_decode(kq.ctx, vq.ctx, q.view(4 * n_kv, group, d), kp, vp, held, keep * block, n_kv_heads=1,
+                            block_table=table, block_size=block)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [x + 1 for x in new] and tq.device_status() == 0
+    tab, sel = pages.block_table.cpu().numpy(), table.cpu().numpy()
+    got, gotp = out.cpu().numpy(), part.cpu().numpy()
+    slots_of = lambda b, h, m: oattn.token_slots(b, h, m, n_kv, block_table=tab)
+    pairs = [(b, h) for b in range(4) for h in (0, 5)]
+    ref = oracle_heads(kq, vq, kp, vp, q.cpu(), pairs, lens.tolist(), slots_of, group)
+    for pr in pairs:
+        assert_attention_close(got[pr][None], ref[pr][None])
+    pairs = [(r, g) for r in range(4 * n_kv) for g in (0, 3)]
+    slots_of = lambda b, h, m: oattn.token_slots(b, h, m, 1, block_table=sel)
+    ref = oracle_heads(kq, vq, kp, vp, q.cpu().view(4 * n_kv, group, d), pairs, held.tolist(), slots_of, group)
+    for pr in pairs:
+        assert_attention_close(gotp[pr][None], ref[pr][None])

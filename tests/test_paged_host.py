@@ -1,0 +1,130 @@
+"""Argument checks of the paged-cache calls that need no GPU: every refusal comes from the host, before
+any CUDA call, with a message.  Pointers are host addresses that nothing reads."""
+import ctypes
+
+import pytest
+
+EINVAL, EUNSUPPORTED, OK = 1, 2, 0
+P = 1 << 20  # an aligned address; refused calls never use it
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_vector_06_b200.build import build
+    build()
+    from kv_cache_vector_06_b200 import tq
+    return tq
+
+
+def pages(lib, **over):
+    f = dict(device=0, batch=3, n_kv_heads=2, block_size=16, max_blocks=8, n_blocks=100, block_table=P) | over
+    return ctypes.byref(lib.PagesC(*[f[n] for n, _ in lib.PagesC._fields_]))
+
+
+def extend(lib, pg, **over):
+    a = dict(seq_lens=P, new_lens=P, free=P, n_free=10, head=P, lens_out=P, granted=P, head_out=P, offsets=P, slots=P,
+             n_slots=6) | over
+    return lib.LIB.tq_page_extend(pg, *a.values(), None)
+
+
+def append(lib, pg, **over):
+    a = dict(seq_lens=P, granted=P, offsets=P, k=P, v=P, dtype=1, d=64, n_rows=3, ld=128, kc=P, vc=P, bounds=P) | over
+    return lib.LIB.tq_append_kv(pg, *a.values(), None)
+
+
+def scores(lib, pg, **over):
+    a = dict(seq_lens=P, q=P, dtype=1, hq=8, d=64, bounds=P, out=P) | over
+    return lib.LIB.tq_block_scores(pg, *a.values(), None)
+
+
+def select(lib, pg, **over):
+    a = dict(seq_lens=P, scores=P, keep=4, first=1, last=2, table=P, lens=P) | over
+    return lib.LIB.tq_select_blocks(pg, *a.values(), None)
+
+
+def attend(lib, pg, **over):
+    a = dict(seq_lens=P, max_len=100, q=P, k=P, v=P, dtype=1, hq=8, d=64, scale=0.0, out=P, out_dtype=0, ws=P,
+             ws_bytes=1 << 40) | over
+    return lib.LIB.tq_attend_paged(pg, *a.values(), None)
+
+
+CALLS = [extend, append, scores, select, attend]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_pages_are_checked(lib, call):
+    assert call(lib, None) == EINVAL and b"pages is NULL" in lib.LIB.tq_last_error()
+    for bad in (dict(batch=-1), dict(n_kv_heads=0), dict(block_size=0), dict(max_blocks=0), dict(n_blocks=-1),
+                dict(block_table=None), dict(block_table=P + 2)):
+        assert call(lib, pages(lib, **bad)) == EINVAL, bad
+        assert b"pages" in lib.LIB.tq_last_error()
+    for big in (dict(batch=1 << 30, n_kv_heads=2), dict(n_blocks=1 << 30), dict(max_blocks=1 << 20, block_size=1 << 11)):
+        assert call(lib, pages(lib, **big)) == EUNSUPPORTED, big
+
+
+def test_empty_batch_is_no_work(lib):
+    empty = pages(lib, batch=0, block_table=None)
+    for call in (append, scores, select, attend):
+        assert call(lib, empty) == OK
+
+
+@pytest.mark.parametrize("over", [dict(seq_lens=None), dict(new_lens=None), dict(free=None), dict(head=None),
+                                  dict(lens_out=None), dict(granted=None), dict(head_out=None), dict(offsets=None),
+                                  dict(slots=None), dict(n_free=-1), dict(n_slots=-2), dict(n_slots=5), dict(seq_lens=P + 1),
+                                  dict(offsets=P + 4), dict(slots=P + 4), dict(head=P + 2)])
+def test_extend_refusals(lib, over):
+    assert extend(lib, pages(lib), **over) == EINVAL and lib.LIB.tq_last_error()
+
+
+@pytest.mark.parametrize("over,st", [(dict(seq_lens=None), EINVAL), (dict(granted=None), EINVAL), (dict(offsets=None), EINVAL),
+                                     (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(kc=None), EINVAL),
+                                     (dict(vc=None), EINVAL), (dict(kc=None, vc=None, bounds=None), EINVAL),
+                                     (dict(dtype=7), EINVAL), (dict(d=60), EUNSUPPORTED), (dict(d=0), EUNSUPPORTED),
+                                     (dict(d=264), EUNSUPPORTED), (dict(ld=127), EINVAL), (dict(ld=132), EINVAL),
+                                     (dict(n_rows=-1), EINVAL), (dict(k=P + 8), EINVAL), (dict(bounds=P + 8), EINVAL),
+                                     (dict(kc=P + 8), EINVAL)])
+def test_append_refusals(lib, over, st):
+    assert append(lib, pages(lib), **over) == st and lib.LIB.tq_last_error()
+
+
+@pytest.mark.parametrize("over,st", [(dict(seq_lens=None), EINVAL), (dict(q=None), EINVAL), (dict(bounds=None), EINVAL),
+                                     (dict(out=None), EINVAL), (dict(dtype=2), EINVAL), (dict(hq=7), EINVAL),
+                                     (dict(hq=0), EINVAL), (dict(hq=34), EUNSUPPORTED), (dict(d=12), EUNSUPPORTED),
+                                     (dict(q=P + 4), EINVAL), (dict(out=P + 4), EINVAL), (dict(bounds=P + 2), EINVAL)])
+def test_score_refusals(lib, over, st):
+    assert scores(lib, pages(lib), **over) == st and lib.LIB.tq_last_error()
+
+
+@pytest.mark.parametrize("over,st", [(dict(seq_lens=None), EINVAL), (dict(scores=None), EINVAL), (dict(table=None), EINVAL),
+                                     (dict(lens=None), EINVAL), (dict(keep=0), EINVAL), (dict(first=-1), EINVAL),
+                                     (dict(last=0), EINVAL), (dict(first=3), EINVAL),
+                                     (dict(first=(1 << 31) - 1, last=(1 << 31) - 1), EINVAL),
+                                     (dict(keep=1 << 28), EUNSUPPORTED), (dict(scores=P + 4), EINVAL), (dict(lens=P + 2), EINVAL)])
+def test_select_refusals(lib, over, st):
+    assert select(lib, pages(lib), **over) == st and lib.LIB.tq_last_error()
+
+
+@pytest.mark.parametrize("over,st", [(dict(seq_lens=None), EINVAL), (dict(q=None), EINVAL), (dict(k=None), EINVAL),
+                                     (dict(v=None), EINVAL), (dict(out=None), EINVAL), (dict(max_len=-1), EINVAL),
+                                     (dict(max_len=129), EINVAL), (dict(dtype=3), EINVAL), (dict(dtype=0, out_dtype=1), EINVAL),
+                                     (dict(out_dtype=9), EINVAL), (dict(hq=9), EINVAL), (dict(hq=64), EUNSUPPORTED),
+                                     (dict(d=4), EUNSUPPORTED), (dict(d=512), EUNSUPPORTED), (dict(q=P + 8), EINVAL),
+                                     (dict(out=P + 8), EINVAL), (dict(k=P + 2), EINVAL)])
+def test_attend_refusals(lib, over, st):
+    assert attend(lib, pages(lib), **over) == st and lib.LIB.tq_last_error()
+
+
+def test_attend_workspace(lib):
+    n = ctypes.c_size_t()
+    pg = pages(lib)
+    assert lib.LIB.tq_attend_paged_workspace_size(pg, 100, 8, 64, ctypes.byref(n)) == OK
+    assert lib.LIB.tq_attend_paged_workspace_size(pg, 100, 8, 64, None) == EINVAL
+    assert lib.LIB.tq_attend_paged_workspace_size(pg, 129, 8, 64, ctypes.byref(n)) == EINVAL
+
+
+def test_binding_refuses_host_tensors(lib):
+    import torch
+    with pytest.raises(ValueError):
+        lib.Pages(torch.zeros(2, 3, dtype=torch.int32), 1, 16, 4)
+    with pytest.raises(ValueError):
+        lib.Pages(torch.zeros(3, dtype=torch.int32), 1, 16, 4)
