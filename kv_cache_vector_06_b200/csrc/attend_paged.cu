@@ -1,4 +1,17 @@
 // Decode attention over an uncompressed paged cache (tq_attend_paged).
+//
+//   o = sum_t e^{s_t - m} v_t / sum_t e^{s_t - m},  s_t = scale <q, k_t>,  m a running maximum
+//
+// Bound: 2 d rows of the cache per (token, KV head) against 4 g d flop, a few flop per byte: HBM.  The
+// group's query heads share each row read, so the products run on the tensor cores (mma.sync: the
+// 128-row tiles of tcgen05 would hold at most 16 query heads), and the loads never wait for them.
+//
+// Work is counted in steps of TOK tokens over all (sequence, KV head) rows laid end to end; every worker
+// takes an equal run of steps, so a ragged batch ends at one time whatever its lengths.  A worker is a
+// block of four warps that share a row's steps (long rows) or a single warp (many short rows).  Each
+// warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
+// A row that falls to several workers leaves pieces (m, l, o) in the workspace, joined by a second
+// kernel.
 #include "device_common.cuh"
 
 namespace {
@@ -10,66 +23,599 @@ struct PagedArgs {
   const int32_t *table, *lens;
   const void *q, *k, *v;
   void *out;
+  int4 *owner;   // [workers]: row whose pieces this worker begins, their number (0: none), slots from one to the next
+  float *piece;  // [workers][2][group][d] o, then [group] m, [group] l of each
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void store(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLog2e = 1.44269504088896340736f;
 
-constexpr int kWarps = 8;
+// Rows of d padded to D channels; T the cache's type.  A step's keys and values take 64 D bytes of ring.
+template <typename T, int D>
+struct Shape {
+  static constexpr int kTok = 32 / sizeof(T);             // tokens per step: 16 (bf16) or 8 (fp32)
+  static constexpr int kRow = D * (int)sizeof(T);         // bytes of a padded row
+  static constexpr int kCh = kRow / 16;                   // 16-byte chunks of a row
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kOcc = D == 64 ? 3 : D == 128 ? 2 : 1;  // blocks per SM
+  static constexpr int kStage = 2 * kTok * kRow;
+  static constexpr int kRing = kStages * kStage;          // per warp
+  static constexpr int kSmem = kWarps * kRing;
+};
 
-// One block per (sequence, query head); its warps take tokens in turn, each with its own running
-// maximum m, sum l and output o of the softmax, joined at the end.
-template <typename T, typename O>
-__global__ void __launch_bounds__(32 * kWarps) attend_paged_kernel(PagedArgs a) {
-  constexpr int kPer = kPagedMaxD / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kPagedMaxD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = blockIdx.x;  // b * n_q_heads + hq
-  const int hq = a.heads * a.group;
-  const int b = (int)(r / hq), h = (int)(r - (int64_t)b * hq) / a.group;
-  const int len = min(max(a.lens[b], 0), a.max_len);
-  float q[kPer], o[kPer];
-  for (int i = 0; i < kPer; ++i) {
-    const int c = lane + 32 * i;
-    q[i] = c < a.d ? to_f(static_cast<const T *>(a.q)[r * a.d + c]) * a.scale : 0.f;
-    o[i] = 0.f;
+__device__ __forceinline__ void store1(float *p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], unsigned addr) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16-byte asynchronous copy; `bytes` 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void cp16(unsigned dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(y) : "f"(x));
+  return y;
+}
+// x = hi + lo to 2^-22 of x: each part rounded to TF32's 11 bits.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
+  hi = tf32(__uint_as_float(x));
+  lo = tf32(__uint_as_float(x) - __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return reinterpret_cast<const uint32_t &>(v);
+}
+// The same, leaving what the rounding dropped in lo and hi.
+__device__ __forceinline__ uint32_t take_bf16(float &lo, float &hi) {
+  const uint32_t v = pack_bf16(lo, hi);
+  lo -= __uint_as_float(v << 16);
+  hi -= __uint_as_float(v & 0xffff0000u);
+  return v;
+}
+
+// Swizzles of a row's 16-byte chunks, so that the accesses below touch every bank once: keys are read as
+// four chunks of two rows, bf16 values as one chunk of eight rows, fp32 values as two chunks of every
+// other row.
+__device__ __forceinline__ int key_chunk(int row, int ch) { return ch ^ ((row & 1) << 2); }
+template <typename T>
+__device__ __forceinline__ int value_chunk(int row, int ch) {
+  return sizeof(T) == 2 ? ch ^ (row & 7) : ch ^ (row & 6);
+}
+
+// One warp's stream over the steps of one row, and its softmax state.
+//   WIDE   more than 8 query heads.  Otherwise rows 8 .. 15 of the products' left operand carry the
+//          low-order parts of the same heads' weights (fp32: also of the queries), so that the parts
+//          cost no products of their own.
+//   PARTS  bf16: bf16 parts that a softmax weight is split into, 2 (error 2^-17 of it, under a bf16
+//          output's rounding) or 3 (2^-25)
+template <typename T, int D, bool WIDE, int PARTS>
+struct Stream {
+  using S = Shape<T, D>;
+  static constexpr bool kBf = sizeof(T) == 2;
+  static constexpr int kKg = S::kCh / 4;                        // 64-byte groups of a row
+  static constexpr int kQRegs = kKg * (WIDE ? 8 : 4) * (kBf ? 1 : 2);
+  static constexpr bool kQInRegs = kQRegs <= 64;
+  static constexpr int kQ = kQInRegs ? kKg : 1;
+  static constexpr int kNt = D / 8;
+  static constexpr int kH = WIDE ? 2 : 1;                       // heads per lane: lane / 4 and 8 + lane / 4
+
+  float o[kNt][4], m[kH], l[kH];
+  uint32_t qf[kQ][kH][kBf ? 1 : 2][4];
+
+  // chunk 4 kg + lane % 4 of query head lane / 4 (+ 8): the left operand's part for this lane, the
+  // channels in the order in which the keys' chunk holds them
+  static __device__ __forceinline__ void load_q(uint32_t (&f)[kH][kBf ? 1 : 2][4], const PagedArgs &a, int64_t row, int kg, int lane) {
+    const int ch = 4 * kg + (lane & 3);
+    const int dch = a.d * (int)sizeof(T) / 16;
+#pragma unroll
+    for (int x = 0; x < kH; ++x) {
+      const int hd = (lane >> 2) + 8 * x;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (hd < a.group && ch < dch)
+        v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (row * a.group + hd) * a.d) + ch);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kBf) f[x][0][i] = w[i];
+        else split_tf32(w[i], f[x][0][i], f[x][1][i]);
+      }
+    }
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = warp; t < len; t += kWarps) {
-    const int e = a.table[(int64_t)b * a.max_blocks + t / a.bs];
-    if (e < 0 || e >= a.n_blocks) continue;
-    const int64_t base = (((int64_t)e * a.heads + h) * a.bs + t % a.bs) * a.d;
-    float s = 0.f;
-    for (int i = 0; i < kPer; ++i) {
-      const int c = lane + 32 * i;
-      if (c < a.d) s = fmaf(q[i], to_f(static_cast<const T *>(a.k)[base + c]), s);
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kH; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.f;
+    }
+  }
+
+  // One step: keys at kbase, values at vbase, tokens `valid`.
+  __device__ __forceinline__ void step(const PagedArgs &a, int64_t row, unsigned kbase, unsigned vbase, uint32_t valid, float sc,
+                                       int lane) {
+    constexpr int kT = S::kTok / 8;
+    const int c = lane & 3, r = lane >> 2;
+    float s[kT][4];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+    for (int kg = 0; kg < kKg; ++kg) {
+      if constexpr (!kQInRegs) load_q(qf[0], a, row, kg, lane);
+      const auto &f = qf[kQInRegs ? kg : 0];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        uint32_t k[4];
+        lds128(k, kbase + (8 * t + r) * S::kRow + 16 * key_chunk(r, 4 * kg + c));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (kBf) {
+            if constexpr (WIDE) mma_bf16(s[t], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], k[2 * u], k[2 * u + 1]);
+            else mma_bf16(s[t], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, k[2 * u], k[2 * u + 1]);
+          } else {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(k[2 * u], h0, l0);
+            split_tf32(k[2 * u + 1], h1, l1);
+            if constexpr (WIDE) {
+              mma_tf32(s[t], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
+              mma_tf32(s[t], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
+              mma_tf32(s[t], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
+            } else {
+              mma_tf32(s[t], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
+              mma_tf32(s[t], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
+            }
+          }
+        }
+      }
+    }
+    // logits in units of log2, masked; lane: head r (+ 8), tokens 8 t + 2 c, 8 t + 2 c + 1
+    float p[kH][kT][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = (valid >> (8 * t + 2 * c + i)) & 1u;
+        if constexpr (WIDE) {
+          p[0][t][i] = in ? s[t][i] * sc : -INFINITY;
+          p[kH - 1][t][i] = in ? s[t][2 + i] * sc : -INFINITY;
+        } else {
+          p[0][t][i] = in ? (kBf ? s[t][i] : s[t][i] + s[t][2 + i]) * sc : -INFINITY;
+        }
+      }
+    // The running maximum moves only when a logit passes it by more than 2^8: weights up to 2^8 above
+    // the others' scale cost no precision in fp32, and o is rescaled a few times per row at most.
+    float top[kH];
+    bool move = false;
+#pragma unroll
+    for (int x = 0; x < kH; ++x) {
+      top[x] = p[x][0][0];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) top[x] = fmaxf(top[x], fmaxf(p[x][t][0], p[x][t][1]));
+      top[x] = fmaxf(top[x], __shfl_xor_sync(TQ_FULL_MASK, top[x], 1));
+      top[x] = fmaxf(top[x], __shfl_xor_sync(TQ_FULL_MASK, top[x], 2));
+      move = move || top[x] > m[x] + 8.f;
+    }
+    if (__any_sync(TQ_FULL_MASK, move)) {
+      float f[kH];
+#pragma unroll
+      for (int x = 0; x < kH; ++x) {
+        const float to = fmaxf(m[x], top[x]);
+        f[x] = m[x] == -INFINITY ? 0.f : exp2a(m[x] - to);
+        m[x] = to;
+        l[x] *= f[x];
+      }
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) {
+        o[n][0] *= f[0];
+        o[n][1] *= f[0];
+        o[n][2] *= f[kH - 1];
+        o[n][3] *= f[kH - 1];
+      }
     }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(TQ_FULL_MASK, s, x);
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : __expf(m - mn), p = __expf(s - mn);
-    l = l * f + p;
-    m = mn;
-    for (int i = 0; i < kPer; ++i) {
-      const int c = lane + 32 * i;
-      if (c < a.d) o[i] = fmaf(p, to_f(static_cast<const T *>(a.v)[base + c]), o[i] * f);
+    for (int x = 0; x < kH; ++x) {
+      const float mm = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          p[x][t][i] = exp2a(p[x][t][i] - mm);
+          l[x] += p[x][t][i];
+        }
+    }
+    if constexpr (kBf) {
+      uint32_t w[PARTS][kH][2];
+#pragma unroll
+      for (int x = 0; x < kH; ++x)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < PARTS - 1; ++i) w[i][x][t] = take_bf16(p[x][t][0], p[x][t][1]);
+          w[PARTS - 1][x][t] = pack_bf16(p[x][t][0], p[x][t][1]);
+        }
+#pragma unroll
+      for (int n = 0; n < kNt; n += 2) {
+        uint32_t v[4];
+        ldsm4t(v, vbase + (lane & 15) * S::kRow + 16 * value_chunk<T>(lane & 15, n + (lane >> 4)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (WIDE) {
+#pragma unroll
+            for (int i = PARTS - 1; i >= 0; --i)
+              mma_bf16(o[n + u], w[i][0][0], w[i][kH - 1][0], w[i][0][1], w[i][kH - 1][1], v[2 * u], v[2 * u + 1]);
+          } else {
+            if constexpr (PARTS == 3) mma_bf16(o[n + u], 0u, w[PARTS - 1][0][0], 0u, w[PARTS - 1][0][1], v[2 * u], v[2 * u + 1]);
+            mma_bf16(o[n + u], w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], v[2 * u], v[2 * u + 1]);
+          }
+        }
+      }
+    } else {
+      // left operand: column c is token 2 c, column c + 4 token 2 c + 1
+      uint32_t ph[kH][2], pl[kH][2];
+#pragma unroll
+      for (int x = 0; x < kH; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_tf32(__float_as_uint(p[x][0][i]), ph[x][i], pl[x][i]);
+#pragma unroll
+      for (int g = 0; g < kNt / 4; ++g) {
+        uint32_t v0[4], v1[4];  // four channels of tokens 2 c and 2 c + 1, one per tile
+        lds128(v0, vbase + (2 * c) * S::kRow + 16 * value_chunk<T>(2 * c, 8 * g + r));
+        lds128(v1, vbase + (2 * c + 1) * S::kRow + 16 * value_chunk<T>(2 * c + 1, 8 * g + r));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h0, l0, h1, l1;
+          split_tf32(v0[i], h0, l0);
+          split_tf32(v1[i], h1, l1);
+          float(&acc)[4] = o[4 * g + i];
+          if constexpr (WIDE) {
+            mma_tf32(acc, pl[0][0], pl[kH - 1][0], pl[0][1], pl[kH - 1][1], h0, h1);
+            mma_tf32(acc, ph[0][0], ph[kH - 1][0], ph[0][1], ph[kH - 1][1], l0, l1);
+            mma_tf32(acc, ph[0][0], ph[kH - 1][0], ph[0][1], ph[kH - 1][1], h0, h1);
+          } else {
+            mma_tf32(acc, 0u, ph[0][0], 0u, ph[0][1], l0, l1);
+            mma_tf32(acc, ph[0][0], pl[0][0], ph[0][1], pl[0][1], h0, h1);
+          }
+        }
+      }
     }
   }
-  for (int i = 0; i < kPer; ++i) so[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+
+  // Channel of accumulator (tile n, column i of this lane).
+  static __device__ __forceinline__ int channel(int n, int i, int lane) {
+    return kBf ? 8 * n + 2 * (lane & 3) + i : 32 * (n >> 2) + 8 * (lane & 3) + 4 * i + (n & 3);
   }
+  __device__ __forceinline__ float value(int n, int i, int x) const {
+    return WIDE ? o[n][2 * x + i] : o[n][i] + o[n][2 + i];
+  }
+};
+
+// Steps of one row: at least one, so that every row has a worker to write it.
+__device__ __forceinline__ int row_steps(int len, int max_len, int tok) {
+  len = min(len, max_len);
+  return len <= tok ? 1 : (len - 1) / tok + 1;
+}
+
+template <typename T, int D, bool WIDE, int PARTS, typename O>
+__global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kernel(PagedArgs a) {
+  using S = Shape<T, D>;
+  using St = Stream<T, D, WIDE, PARTS>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t wsum[kWarps];
+  __shared__ int64_t at_pos[kWarps];
+  __shared__ int at_seq[kWarps];
+  __shared__ uint32_t masks[kWarps][S::kStages];
+  __shared__ float mm[kWarps][16], ll[kWarps][16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  // ---- the batch's steps: each thread sums a run of sequences, then a block scan
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int64_t b0 = min((int64_t)threadIdx.x * per, (int64_t)a.batch), b1 = min(b0 + per, (int64_t)a.batch);
+  int64_t mine = 0;
+  for (int64_t b = b0; b < b1; ++b) mine += row_steps(a.lens[b], a.max_len, S::kTok);
+  mine *= a.heads;
+  int64_t incl = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int64_t u = __shfl_up_sync(TQ_FULL_MASK, incl, x);
+    if (lane >= x) incl += u;
+  }
+  if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < kWarps; ++w) L += sl[w] > 0.f ? sl[w] * __expf(sm[w] - M) : 0.f;
-  for (int c = threadIdx.x; c < a.d; c += 32 * kWarps) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += sl[w] > 0.f ? so[w][c] * __expf(sm[w] - M) : 0.f;
-    store(static_cast<O *>(a.out) + r * a.d + c, L > 0.f ? x / L : 0.f);
+  int64_t total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += wsum[w];
+    total += wsum[w];
+  }
+  // ---- workers
+  const int64_t rows = (int64_t)a.batch * a.heads;
+  const bool solo = rows >= (int64_t)gridDim.x && total < 8 * rows;
+  const int team = solo ? 1 : kWarps;
+  int64_t workers = solo ? (int64_t)gridDim.x * kWarps : (int64_t)gridDim.x;
+  workers = max((int64_t)1, min(workers, total / (solo ? 1 : kWarps)));
+  for (int w = 0; w < kWarps; w += team) {
+    const int64_t id = solo ? (int64_t)blockIdx.x * kWarps + w : (int64_t)blockIdx.x;
+    if (id < workers) {
+      const int64_t pos = total * id / workers;
+      if (mine > 0 && pos >= before && pos < before + mine) {
+        int64_t left = pos - before;
+        int64_t b = b0;
+        for (;; ++b) {
+          const int64_t n = (int64_t)row_steps(a.lens[b], a.max_len, S::kTok) * a.heads;
+          if (left < n) break;
+          left -= n;
+        }
+        at_seq[w] = (int)b;
+        at_pos[w] = left;
+      }
+    }
+  }
+  if (lane == 0) a.owner[blockIdx.x * kWarps + warp] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  const int lead = solo ? warp : 0;  // first warp of the team
+  const int slot0 = blockIdx.x * kWarps + lead;
+  const int64_t id = solo ? (int64_t)slot0 : (int64_t)blockIdx.x;
+  if (id >= workers) return;
+  const int64_t begin = total * id / workers, end = total * (id + 1) / workers;
+  int b = at_seq[lead], len, steps;
+  auto enter = [&](int seq) {
+    len = min(max(a.lens[seq], 0), a.max_len);
+    steps = row_steps(len, a.max_len, S::kTok);
+  };
+  enter(b);
+  int h = (int)(at_pos[lead] / steps), first = (int)(at_pos[lead] - (int64_t)h * steps);
+
+  const unsigned ring = smem_addr(smem) + warp * S::kRing;
+  const int esz_row = a.d * (int)sizeof(T);  // bytes of a row in the cache
+  const int dch = esz_row / 16;
+  const bool whole = a.bs % S::kTok == 0;  // a step lies in one block
+  const float sc = a.scale * kLog2e;
+  const int rank = solo ? 0 : warp;
+  St st;
+
+  for (int64_t pos = begin; pos < end;) {
+    const int count = (int)min((int64_t)(steps - first), end - pos);
+    const int64_t row = (int64_t)b * a.heads + h;
+    const int32_t *table = a.table + (int64_t)b * a.max_blocks;
+    const int n = (count - rank + team - 1) / team;
+    // block of this lane's token (of the whole step where it lies in one block)
+    auto entry = [&](int i) {
+      const int t = (first + rank + i * team) * S::kTok + (whole ? 0 : (lane & (S::kTok - 1)));
+      return i < n && t < len ? __ldg(table + t / a.bs) : -1;
+    };
+    auto issue = [&](int i, int e) {
+      const int stage = i % S::kStages;
+      const int t0 = (first + rank + i * team) * S::kTok;
+      const bool ok = e >= 0 && e < a.n_blocks;
+      const int t = t0 + (whole ? 0 : (lane & (S::kTok - 1)));
+      const int64_t off = ok ? (((int64_t)e * a.heads + h) * a.bs + t % a.bs) * esz_row : 0;
+      uint32_t valid = __ballot_sync(TQ_FULL_MASK, whole ? ok && t0 + lane < len : ok);
+      valid &= (1u << S::kTok) - 1u;
+      if (lane == 0) masks[warp][stage] = valid;
+      const unsigned kb = ring + stage * S::kStage, vb = kb + S::kTok * S::kRow;
+#pragma unroll
+      for (int x = 0; x < S::kTok * S::kCh / 32; ++x) {
+        const int idx = lane + 32 * x, r = idx / S::kCh, ch = idx % S::kCh;
+        const int64_t base = whole ? off + (int64_t)r * esz_row : __shfl_sync(TQ_FULL_MASK, off, r);
+        const bool in = ((valid >> r) & 1u) && ch < dch;
+        const int64_t src = in ? base + 16 * ch : 0;
+        cp16(kb + r * S::kRow + 16 * key_chunk(r, ch), static_cast<const char *>(a.k) + src, in ? 16 : 0);
+        cp16(vb + r * S::kRow + 16 * value_chunk<T>(r, ch), static_cast<const char *>(a.v) + src, in ? 16 : 0);
+      }
+    };
+    int e[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      if (i < n) issue(i, e[i]);
+      cp_commit();
+    }
+    int next = e[S::kStages - 1];
+    if constexpr (St::kQInRegs) {
+#pragma unroll
+      for (int kg = 0; kg < St::kKg; ++kg) St::load_q(st.qf[kg], a, row, kg, lane);
+    }
+    st.clear();
+    for (int i = 0; i < n; ++i) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();  // this step's copies of every lane have landed; the last step's stage is free
+      if (i + S::kStages - 1 < n) issue(i + S::kStages - 1, next);
+      cp_commit();
+      next = entry(i + S::kStages);
+      const int stage = i % S::kStages;
+      const unsigned kb = ring + stage * S::kStage;
+      st.step(a, row, kb, kb + S::kTok * S::kRow, masks[warp][stage], sc, lane);
+    }
+    cp_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < St::kH; ++x) {
+      st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 1);
+      st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 2);
+    }
+
+    // ---- the row's end, or the worker's: the output, or a piece of it
+    const bool starts = first == 0, ends = first + count == steps;
+    const int g = a.group;
+    float *piece = a.piece + ((int64_t)slot0 * 2 + (starts ? 1 : 0)) * g * (a.d + 2);
+    if (solo) {
+#pragma unroll
+      for (int x = 0; x < St::kH; ++x) {
+        const int hd = (lane >> 2) + 8 * x;
+        if (hd >= g) continue;
+        if (starts && ends) {
+          const float inv = st.l[x] > 0.f ? 1.f / st.l[x] : 0.f;
+          O *out = static_cast<O *>(a.out) + (row * g + hd) * a.d;
+#pragma unroll
+          for (int t = 0; t < St::kNt; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c = St::channel(t, i, lane);
+              if (c < a.d) store1(out + c, st.value(t, i, x) * inv);
+            }
+        } else {
+#pragma unroll
+          for (int t = 0; t < St::kNt; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c = St::channel(t, i, lane);
+              if (c < a.d) piece[hd * a.d + c] = st.value(t, i, x);
+            }
+          if ((lane & 3) == 0) {
+            piece[g * a.d + hd] = st.m[x];
+            piece[g * a.d + g + hd] = st.l[x];
+          }
+        }
+      }
+    } else {
+      float *buf = reinterpret_cast<float *>(smem) + warp * 16 * D;
+      __syncthreads();  // every warp's ring is drained: its shared memory holds the warps' sums now
+#pragma unroll
+      for (int x = 0; x < St::kH; ++x) {
+        const int hd = (lane >> 2) + 8 * x;
+        if (hd >= g) continue;
+#pragma unroll
+        for (int t = 0; t < St::kNt; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) buf[hd * D + St::channel(t, i, lane)] = st.value(t, i, x);
+        if ((lane & 3) == 0) {
+          mm[warp][hd] = st.m[x];
+          ll[warp][hd] = st.l[x];
+        }
+      }
+      __syncthreads();
+      for (int idx = threadIdx.x; idx < g * D; idx += kThreads) {
+        const int hd = idx / D, c = idx % D;
+        float top = -INFINITY, sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mm[w][hd]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = mm[w][hd] == -INFINITY ? 0.f : exp2a(mm[w][hd] - top);
+          sum = fmaf(f, ll[w][hd], sum);
+          x = fmaf(f, reinterpret_cast<const float *>(smem)[(w * 16 + hd) * D + c], x);
+        }
+        if (c >= a.d) continue;
+        if (starts && ends) {
+          store1(static_cast<O *>(a.out) + (row * g + hd) * a.d + c, sum > 0.f ? x / sum : 0.f);
+        } else {
+          piece[hd * a.d + c] = x;
+          if (c == 0) {
+            piece[g * a.d + hd] = top;
+            piece[g * a.d + g + hd] = sum;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (starts && !ends && rank == 0 && lane == 0) {
+      // the row's last step decides how many workers hold pieces of it
+      const int64_t last = pos + steps - 1;
+      int64_t to = last * workers / total;
+      while (total * (to + 1) / workers <= last) ++to;
+      while (total * to / workers > last) --to;
+      a.owner[slot0] = make_int4((int)row, (int)(to - id + 1), solo ? 1 : kWarps, 0);
+    }
+
+    pos += count;
+    first = 0;
+    if (pos < end && ++h == a.heads) {
+      h = 0;
+      enter(++b);
+    }
+  }
+}
+
+// Joins the pieces of rows that several workers shared.  Block (x, head): the rows that block x of the
+// kernel above began; its warps take pieces in turn, lanes four channels each.
+constexpr int kMergeWarps = 8;
+template <typename O>
+__global__ void __launch_bounds__(32 * kMergeWarps) attend_paged_merge_kernel(PagedArgs a) {
+  __shared__ float sm[kMergeWarps], sl[kMergeWarps];
+  __shared__ __align__(16) float so[kMergeWarps][kPagedMaxD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hd = blockIdx.y, g = a.group;
+  const int64_t stride = (int64_t)g * (a.d + 2);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  for (int w = 0; w < kWarps; ++w) {
+    const int slot = blockIdx.x * kWarps + w;
+    const int4 own = a.owner[slot];
+    if (own.y == 0) continue;
+    float m = -INFINITY, l = 0.f, o[kPagedMaxD / 32];
+#pragma unroll
+    for (int i = 0; i < kPagedMaxD / 32; ++i) o[i] = 0.f;
+    for (int p = warp; p < own.y; p += kMergeWarps) {
+      const float *piece = a.piece + ((int64_t)(slot + p * own.z) * 2 + (p == 0 ? 1 : 0)) * stride;
+      const float pm = piece[g * a.d + hd], pl = piece[g * a.d + g + hd];
+      const float to = fmaxf(m, pm);
+      if (to == -INFINITY) continue;
+      const float f0 = exp2a(m - to), f1 = exp2a(pm - to);
+      m = to;
+      l = l * f0 + pl * f1;
+#pragma unroll
+      for (int i = 0; i < kPagedMaxD / 32; ++i) {
+        const int c = lane + 32 * i;
+        if (c < a.d) o[i] = o[i] * f0 + piece[hd * a.d + c] * f1;
+      }
+    }
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < kPagedMaxD / 32; ++i) so[warp][lane + 32 * i] = o[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.d; c += 32 * kMergeWarps) {
+      float top = -INFINITY, sum = 0.f, x = 0.f;
+      for (int v = 0; v < kMergeWarps; ++v) top = fmaxf(top, sm[v]);
+      for (int v = 0; v < kMergeWarps; ++v) {
+        const float f = sm[v] == -INFINITY ? 0.f : exp2a(sm[v] - top);
+        sum = fmaf(f, sl[v], sum);
+        x = fmaf(f, so[v][c], x);
+      }
+      store1(static_cast<O *>(a.out) + ((int64_t)own.x * g + hd) * a.d + c, sum > 0.f ? x / sum : 0.f);
+    }
+    __syncthreads();
   }
 }
 
@@ -88,6 +634,61 @@ tq_status check_attend(const tq_pages *pages, int32_t max_seq_len, int32_t n_q_h
   return TQ_OK;
 }
 
+// Blocks of the attention kernel: as many as fit on the GPU at once, fewer where the rows could not give
+// each a step per warp.  The same for both cache types (8 tokens per step counted for bf16 too), so that
+// one workspace size serves them.
+int attend_grid(const tq_pages &p, int32_t max_seq_len, int32_t d) {
+  const int occ = d <= 64 ? Shape<float, 64>::kOcc : d <= 128 ? Shape<float, 128>::kOcc : Shape<float, 256>::kOcc;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p.device) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();
+    sms = 148;
+  }
+  const int64_t steps = (int64_t)p.batch * p.n_kv_heads * (max_seq_len <= 8 ? 1 : (max_seq_len - 1) / 8 + 1);
+  const int64_t want = (steps + kWarps - 1) / kWarps, most = (int64_t)occ * sms;
+  return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+size_t owner_bytes(int grid) { return (size_t)tq_align_up((int64_t)grid * kWarps * sizeof(int4), 256); }
+
+template <typename T, int D, bool WIDE, int PARTS, typename O>
+cudaError_t launch(const PagedArgs &a, int grid, cudaStream_t st) {
+  using S = Shape<T, D>;
+  auto kern = attend_paged_kernel<T, D, WIDE, PARTS, O>;
+  cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
+  if (e != cudaSuccess) return e;
+  tq_prof_begin(TQK_ATTEND_PAGED, st);
+  kern<<<grid, kThreads, S::kSmem, st>>>(a);
+  tq_prof_end(TQK_ATTEND_PAGED, st);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 mgrid((unsigned)grid, (unsigned)a.group);
+  if (tq_prof_on()) {
+    tq_prof_begin(TQK_ATTEND_PAGED_MERGE, st);
+    attend_paged_merge_kernel<O><<<mgrid, 32 * kMergeWarps, 0, st>>>(a);
+    tq_prof_end(TQK_ATTEND_PAGED_MERGE, st);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = mgrid;
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_paged_merge_kernel<O>, a);
+}
+
+template <typename T, int PARTS, typename O>
+cudaError_t launch_d(const PagedArgs &a, int grid, cudaStream_t st) {
+  const bool wide = a.group > 8;
+  if (a.d <= 64) return wide ? launch<T, 64, true, PARTS, O>(a, grid, st) : launch<T, 64, false, PARTS, O>(a, grid, st);
+  if (a.d <= 128) return wide ? launch<T, 128, true, PARTS, O>(a, grid, st) : launch<T, 128, false, PARTS, O>(a, grid, st);
+  return wide ? launch<T, 256, true, PARTS, O>(a, grid, st) : launch<T, 256, false, PARTS, O>(a, grid, st);
+}
+
 }  // namespace
 
 extern "C" tq_status tq_attend_paged_workspace_size(const tq_pages *pages, int32_t max_seq_len, int32_t n_q_heads,
@@ -95,7 +696,8 @@ extern "C" tq_status tq_attend_paged_workspace_size(const tq_pages *pages, int32
   tq_status st = check_attend(pages, max_seq_len, n_q_heads, d);
   if (st != TQ_OK) return st;
   if (!bytes) return tq_fail(TQ_EINVAL, "bytes is NULL");
-  *bytes = 0;
+  const int grid = attend_grid(*pages, max_seq_len, d);
+  *bytes = owner_bytes(grid) + sizeof(float) * 2 * (size_t)grid * kWarps * (n_q_heads / pages->n_kv_heads) * (d + 2);
   return TQ_OK;
 }
 
@@ -124,12 +726,12 @@ extern "C" tq_status tq_attend_paged(const tq_pages *pages, const int32_t *seq_l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedArgs a{pages->batch, pages->n_kv_heads, n_q_heads / pages->n_kv_heads, pages->block_size, pages->max_blocks,
               max_seq_len, d, pages->n_blocks, scale != 0.f ? scale : 1.f / sqrtf((float)d), pages->block_table, seq_lens,
-              q, k_cache, v_cache, out};
-  const unsigned grid = (unsigned)(pages->batch * n_q_heads);
-  tq_prof_begin(TQK_ATTEND_PAGED, s);
-  if (dtype == TQ_F32) attend_paged_kernel<float, float><<<grid, 32 * kWarps, 0, s>>>(a);
-  else if (out_dtype == TQ_F32) attend_paged_kernel<__nv_bfloat16, float><<<grid, 32 * kWarps, 0, s>>>(a);
-  else attend_paged_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 32 * kWarps, 0, s>>>(a);
-  tq_prof_end(TQK_ATTEND_PAGED, s);
-  return tq_cuda_check(cudaGetLastError(), "paged attention launch");
+              q, k_cache, v_cache, out, nullptr, nullptr};
+  const int grid = attend_grid(*pages, max_seq_len, d);
+  a.owner = static_cast<int4 *>(ws);
+  a.piece = reinterpret_cast<float *>(static_cast<char *>(ws) + owner_bytes(grid));
+  cudaError_t e = dtype == TQ_F32       ? launch_d<float, 2, float>(a, grid, s)
+                  : out_dtype == TQ_F32 ? launch_d<__nv_bfloat16, 3, float>(a, grid, s)
+                                        : launch_d<__nv_bfloat16, 2, __nv_bfloat16>(a, grid, s);
+  return tq_cuda_check(e, "paged attention launch");
 }
