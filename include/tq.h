@@ -327,8 +327,8 @@ tq_status tq_search_topk(const tq_ctx *ctx, const void *q, tq_dtype dtype, int32
  *   n_blocks     physical blocks; table entries outside [0, n_blocks) name no block: their tokens
  *                get no slot, are not written, and take no part in attention
  *   block_table  device int32 [batch][max_blocks]
- * Supported: batch * n_kv_heads and n_blocks * n_kv_heads up to 2^31 - 1, max_blocks * block_size up
- * to 2^31 - 1.  Lengths are device int32 [batch]; negative ones count as 0, and those past
+ * Supported: n_kv_heads up to 65535, batch * n_kv_heads and n_blocks * n_kv_heads up to 2^31 - 1,
+ * max_blocks * block_size up to 2^30.  Lengths are device int32 [batch]; negative ones count as 0, and those past
  * max_blocks * block_size as that.  None of these calls synchronizes or allocates. */
 typedef struct {
   int32_t device;

@@ -12,7 +12,7 @@
 // warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
 // A row that falls to several workers leaves pieces (m, l, o) in the workspace, joined by a second
 // kernel.
-#include "device_common.cuh"
+#include "paged_device.cuh"
 
 namespace {
 
@@ -27,93 +27,10 @@ struct PagedArgs {
   float *piece;  // [workers][2][group][d] o, then [group] m, [group] l of each
 };
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.44269504088896340736f;
-
-// Rows of d padded to D channels; T the cache's type.  A step's keys and values take 64 D bytes of ring.
-template <typename T, int D>
-struct Shape {
-  static constexpr int kTok = 32 / sizeof(T);             // tokens per step: 16 (bf16) or 8 (fp32)
-  static constexpr int kRow = D * (int)sizeof(T);         // bytes of a padded row
-  static constexpr int kCh = kRow / 16;                   // 16-byte chunks of a row
-  static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kOcc = D == 64 ? 3 : D == 128 ? 2 : 1;  // blocks per SM
-  static constexpr int kStage = 2 * kTok * kRow;
-  static constexpr int kRing = kStages * kStage;          // per warp
-  static constexpr int kSmem = kWarps * kRing;
-};
 
 __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void lds128(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-// 16-byte asynchronous copy; `bytes` 0 fills with zeros and reads nothing.
-__device__ __forceinline__ void cp16(unsigned dst, const void *src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ float exp2a(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t y;
-  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(y) : "f"(x));
-  return y;
-}
-// x = hi + lo to 2^-22 of x: each part rounded to TF32's 11 bits.
-__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-  hi = tf32(__uint_as_float(x));
-  lo = tf32(__uint_as_float(x) - __uint_as_float(hi));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return reinterpret_cast<const uint32_t &>(v);
-}
-// The same, leaving what the rounding dropped in lo and hi.
-__device__ __forceinline__ uint32_t take_bf16(float &lo, float &hi) {
-  const uint32_t v = pack_bf16(lo, hi);
-  lo -= __uint_as_float(v << 16);
-  hi -= __uint_as_float(v & 0xffff0000u);
-  return v;
-}
-
-// Swizzles of a row's 16-byte chunks, so that the accesses below touch every bank once: keys are read as
-// four chunks of two rows, bf16 values as one chunk of eight rows, fp32 values as two chunks of every
-// other row.
-__device__ __forceinline__ int key_chunk(int row, int ch) { return ch ^ ((row & 1) << 2); }
-template <typename T>
-__device__ __forceinline__ int value_chunk(int row, int ch) {
-  return sizeof(T) == 2 ? ch ^ (row & 7) : ch ^ (row & 6);
-}
 
 // One warp's stream over the steps of one row, and its softmax state.
 //   WIDE   more than 8 query heads.  Otherwise rows 8 .. 15 of the products' left operand carry the
@@ -134,26 +51,6 @@ struct Stream {
 
   float o[kNt][4], m[kH], l[kH];
   uint32_t qf[kQ][kH][kBf ? 1 : 2][4];
-
-  // chunk 4 kg + lane % 4 of query head lane / 4 (+ 8): the left operand's part for this lane, the
-  // channels in the order in which the keys' chunk holds them
-  static __device__ __forceinline__ void load_q(uint32_t (&f)[kH][kBf ? 1 : 2][4], const PagedArgs &a, int64_t row, int kg, int lane) {
-    const int ch = 4 * kg + (lane & 3);
-    const int dch = a.d * (int)sizeof(T) / 16;
-#pragma unroll
-    for (int x = 0; x < kH; ++x) {
-      const int hd = (lane >> 2) + 8 * x;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (hd < a.group && ch < dch)
-        v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (row * a.group + hd) * a.d) + ch);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kBf) f[x][0][i] = w[i];
-        else split_tf32(w[i], f[x][0][i], f[x][1][i]);
-      }
-    }
-  }
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -179,7 +76,7 @@ struct Stream {
       for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
     for (int kg = 0; kg < kKg; ++kg) {
-      if constexpr (!kQInRegs) load_q(qf[0], a, row, kg, lane);
+      if constexpr (!kQInRegs) load_q<T, kH>(qf[0], a.q, row, a.group, a.d, kg, lane);
       const auto &f = qf[kQInRegs ? kg : 0];
 #pragma unroll
       for (int t = 0; t < kT; ++t) {
@@ -327,46 +224,21 @@ struct Stream {
   }
 };
 
-// Steps of one row: at least one, so that every row has a worker to write it.
-__device__ __forceinline__ int row_steps(int len, int max_len, int tok) {
-  len = min(len, max_len);
-  return len <= tok ? 1 : (len - 1) / tok + 1;
-}
-
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kernel(PagedArgs a) {
   using S = Shape<T, D>;
   using St = Stream<T, D, WIDE, PARTS>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t wsum[kWarps];
   __shared__ int64_t at_pos[kWarps];
   __shared__ int at_seq[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
   __shared__ float mm[kWarps][16], ll[kWarps][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  // ---- the batch's steps: each thread sums a run of sequences, then a block scan
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int64_t b0 = min((int64_t)threadIdx.x * per, (int64_t)a.batch), b1 = min(b0 + per, (int64_t)a.batch);
-  int64_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += row_steps(a.lens[b], a.max_len, S::kTok);
-  mine *= a.heads;
-  int64_t incl = mine;
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const int64_t u = __shfl_up_sync(TQ_FULL_MASK, incl, x);
-    if (lane >= x) incl += u;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
-  }
+  StepScan scan;
+  scan.run(a.lens, a.batch, a.heads, a.max_len, S::kTok);
+  const int64_t total = scan.total;
   // ---- workers
   const int64_t rows = (int64_t)a.batch * a.heads;
   const bool solo = rows >= (int64_t)gridDim.x && total < 8 * rows;
@@ -376,18 +248,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
   for (int w = 0; w < kWarps; w += team) {
     const int64_t id = solo ? (int64_t)blockIdx.x * kWarps + w : (int64_t)blockIdx.x;
     if (id < workers) {
-      const int64_t pos = total * id / workers;
-      if (mine > 0 && pos >= before && pos < before + mine) {
-        int64_t left = pos - before;
-        int64_t b = b0;
-        for (;; ++b) {
-          const int64_t n = (int64_t)row_steps(a.lens[b], a.max_len, S::kTok) * a.heads;
-          if (left < n) break;
-          left -= n;
-        }
-        at_seq[w] = (int)b;
-        at_pos[w] = left;
-      }
+      scan.find(total * id / workers, a.lens, a.max_len, S::kTok, at_seq[w], at_pos[w]);
     }
   }
   if (lane == 0) a.owner[blockIdx.x * kWarps + warp] = make_int4(0, 0, 0, 0);
@@ -454,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
     int next = e[S::kStages - 1];
     if constexpr (St::kQInRegs) {
 #pragma unroll
-      for (int kg = 0; kg < St::kKg; ++kg) St::load_q(st.qf[kg], a, row, kg, lane);
+      for (int kg = 0; kg < St::kKg; ++kg) load_q<T, St::kH>(st.qf[kg], a.q, row, a.group, a.d, kg, lane);
     }
     st.clear();
     for (int i = 0; i < n; ++i) {

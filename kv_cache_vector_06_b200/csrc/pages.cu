@@ -1,7 +1,7 @@
 // Paged-cache bookkeeping: block tables, lengths and slot maps from request lengths
 // (tq_page_extend), and the append of uncompressed rows with the channel bounds of every block's
 // keys (tq_append_kv).
-#include "device_common.cuh"
+#include "paged_device.cuh"
 
 tq_status tq_check_pages(const tq_pages *p) {
   tq_fail(TQ_OK, "%s", "");
@@ -12,9 +12,10 @@ tq_status tq_check_pages(const tq_pages *p) {
   if (p->batch > 0 && !p->block_table) return tq_fail(TQ_EINVAL, "pages: block_table is NULL");
   if (!tq_aligned(p->block_table, 4)) return tq_fail(TQ_EINVAL, "pages: block_table not 4-byte aligned");
   if ((int64_t)p->batch * p->n_kv_heads > INT32_MAX || p->n_blocks > INT32_MAX / p->n_kv_heads ||
-      (int64_t)p->max_blocks * p->block_size > INT32_MAX)
+      (int64_t)p->max_blocks * p->block_size > kPagedMaxTokens || p->n_kv_heads > kPagedMaxHeads)
     return tq_fail(TQ_EUNSUPPORTED,
-                   "pages: batch * n_kv_heads, n_blocks * n_kv_heads and max_blocks * block_size must be below 2^31");
+                   "pages: n_kv_heads up to %d, batch * n_kv_heads and n_blocks * n_kv_heads below 2^31, "
+                   "max_blocks * block_size up to 2^30", kPagedMaxHeads);
   return TQ_OK;
 }
 
@@ -35,149 +36,210 @@ tq_status tq_check_group(const tq_pages &p, int32_t n_q_heads) {
 
 namespace {
 
-constexpr int kExtendThreads = 1024;
+constexpr int kExtendThreads = 512;
 
-// Exclusive prefix sums of two values over the block's threads; totals in every thread.  Sums are
-// int64: lengths are arbitrary int32 values.
-__device__ __forceinline__ void block_scan2(int64_t a, int64_t b, int64_t &ea, int64_t &eb, int64_t &ta, int64_t &tb) {
-  __shared__ int64_t wa[32], wb[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int64_t sa = a, sb = b;
+// Exclusive prefix sum over the block's threads, and the total.  int64: lengths are any int32 values.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total) {
+  __shared__ int64_t w[kExtendThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t ua = __shfl_up_sync(TQ_FULL_MASK, sa, o), ub = __shfl_up_sync(TQ_FULL_MASK, sb, o);
-    if (lane >= o) {
-      sa += ua;
-      sb += ub;
-    }
+    const int64_t u = __shfl_up_sync(TQ_FULL_MASK, s, o);
+    if (lane >= o) s += u;
   }
-  if (lane == 31) {
-    wa[warp] = sa;
-    wb[warp] = sb;
+  if (lane == 31) w[warp] = s;
+  __syncthreads();
+  int64_t p = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kExtendThreads / 32; ++i) {
+    const int64_t x = w[i];
+    if (i < warp) p += x;
+    total += x;
   }
   __syncthreads();
-  int64_t pa = 0, pb = 0;
-  ta = tb = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w < warp) {
-      pa += wa[w];
-      pb += wb[w];
-    }
-    ta += wa[w];
-    tb += wb[w];
-  }
-  __syncthreads();
-  ea = pa + sa - a;
-  eb = pb + sb - b;
+  return p + s - v;
 }
 
 struct ExtendArgs {
   int batch, heads, bs, max_blocks, n_free;
-  int64_t n_blocks, n_rows, n_slots;
+  int64_t n_blocks, n_rows;
   int32_t *table;
   const int32_t *lens, *grow, *free_blocks, *free_head;
   int32_t *lens_out, *granted, *free_head_out;
   int64_t *offsets, *slots;
+  FastDiv by_heads, by_bs;
 };
 
-// One block: prefix sums of the new rows and of the needed blocks over the batch, a chunk of
-// kExtendThreads sequences at a time.  The needed blocks of a sequence that the free list cannot
-// serve stay in the sum, so every later one that needs a block is refused too and the blocks taken
-// are a run of the free list.
+// What one sequence of the current chunk needs for its slots.
+struct Grown {
+  int before;  // tokens held
+  int have;    // blocks held
+  int at;      // entry of the free list of its first new block
+  int ok;
+};
+
+// Prefix sums of the new rows and of the needed blocks over the batch, a chunk of kExtendThreads
+// sequences at a time.  The needed blocks of a sequence that the free list cannot serve stay in the sum,
+// so every later one that needs a block is refused too and the blocks taken are a run of the free list.
+//
+// SLOTS: this block writes the slots and table entries of its equal share of the rows.  A few tokens per
+// sequence take one block that does both halves; for whole prompts every block of a large grid repeats
+// the scan (a microsecond) and writes its share, 8 bytes per (row, head), and STATE, the lengths and
+// counters, follows in a second launch: they may be updated in place, after every block has read them.
+template <bool SLOTS, bool STATE>
 __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs a) {
+  __shared__ int64_t first_row[kExtendThreads + 1];
+  __shared__ Grown grown[kExtendThreads];
   int64_t rows0 = 0, need0 = 0;  // sums before this chunk
   int64_t taken = 0;             // blocks granted, this thread's sequences
   const int64_t most = (int64_t)a.max_blocks * a.bs;
+  if (!SLOTS) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  else asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int64_t head = min(max((int64_t)*a.free_head, (int64_t)0), (int64_t)a.n_free);
+  const int64_t lo = a.n_rows * blockIdx.x / gridDim.x, hi = a.n_rows * (blockIdx.x + 1) / gridDim.x;
   for (int b0 = 0; b0 < a.batch; b0 += kExtendThreads) {
     const int b = b0 + threadIdx.x;
     const bool in = b < a.batch;
     const int64_t len = in ? max(a.lens[b], 0) : 0, add = in ? max(a.grow[b], 0) : 0;
     const int64_t have = (len + a.bs - 1) / a.bs;
-    int64_t row, rows_total, upto, need_total;
     // the rows' offsets decide which sequences fit, so they come before the blocks' sum
-    int64_t unused, unused_total;
-    block_scan2(add, 0, row, unused, rows_total, unused_total);
-    row += rows0;
+    int64_t rows_total, need_total;
+    const int64_t row = rows0 + block_scan(add, rows_total);
     const bool fits = len + add <= most && row + add <= a.n_rows;
     const int64_t need = in && fits ? (len + add + a.bs - 1) / a.bs - have : 0;
-    block_scan2(need, 0, upto, unused, need_total, unused_total);
-    upto += need0;
+    const int64_t upto = need0 + block_scan(need, need_total);
     const bool ok = fits && (need == 0 || head + upto + need <= a.n_free);
-    if (in) {
+    if (STATE && in) {
       a.offsets[b] = row;
       a.granted[b] = ok ? (int32_t)add : 0;
       a.lens_out[b] = (int32_t)(ok ? len + add : len);
-      if (ok) {
-        taken += need;
-        for (int64_t i = 0; i < need; ++i)
-          a.table[(int64_t)b * a.max_blocks + have + i] = a.free_blocks[head + upto + i];
+      if (ok) taken += need;
+    }
+    if (SLOTS && rows0 < hi && rows0 + rows_total > lo) {
+      const int count = min(kExtendThreads, a.batch - b0);
+      first_row[threadIdx.x] = row;
+      if (threadIdx.x == 0) first_row[count] = rows0 + rows_total;
+      // a sequence that is not grown is never asked for its other values
+      grown[threadIdx.x] = Grown{(int)len, (int)have, (int)(ok ? head + upto : 0), ok && add > 0};
+      __syncthreads();
+      const int64_t r0 = max(lo, rows0), r1 = min(hi, rows0 + rows_total);
+      // (rows of a block) x heads stays below 2^31 in a pass of this many rows
+      const int64_t pass = max((int64_t)1, (int64_t)(1 << 30) / a.heads);
+      for (int64_t p0 = r0; p0 < r1; p0 += pass) {
+        const int n = (int)(min(r1, p0 + pass) - p0) * a.heads;
+        int s = 0;  // sequence of the last row looked up: rows come in order
+        int64_t s_lo = 1, s_hi = 0;
+        for (int i = threadIdx.x; i < n; i += kExtendThreads) {
+          const int k = a.by_heads(i), h = i - k * a.heads;
+          const int64_t r = p0 + k;
+          if (r < s_lo || r >= s_hi) {
+            int u = 0, v = count;  // first_row[u] <= r < first_row[v]
+            while (v - u > 1) {
+              const int mid = (u + v) >> 1;
+              if (first_row[mid] <= r) u = mid;
+              else v = mid;
+            }
+            s = u;
+            s_lo = first_row[u];
+            s_hi = first_row[u + 1];
+          }
+          const Grown g = grown[s];
+          int64_t slot = -1;
+          if (g.ok) {
+            const int pos = g.before + (int)(r - s_lo), j = a.by_bs(pos), off = pos - j * a.bs;
+            int32_t *entry = a.table + (int64_t)(b0 + s) * a.max_blocks + j;
+            int e;
+            if (j >= g.have) {
+              e = __ldg(a.free_blocks + g.at + (j - g.have));
+              if (off == 0 && h == 0) *entry = e;  // a new block begins with a new row
+            } else {
+              e = *entry;
+            }
+            if (e >= 0 && e < a.n_blocks) slot = ((int64_t)e * a.heads + h) * a.bs + off;
+          }
+          a.slots[p0 * a.heads + i] = slot;
+        }
       }
+      __syncthreads();
     }
     rows0 += rows_total;
     need0 += need_total;
   }
-  int64_t ea, eb, total, unused;
-  block_scan2(taken, 0, ea, eb, total, unused);
-  if (threadIdx.x == 0) {
-    a.offsets[a.batch] = rows0;
-    *a.free_head_out = (int32_t)(head + total);
-  }
-}
-
-// Last sequence whose rows begin at or before `row` and do not end there (row < offsets[batch]).
-__device__ __forceinline__ int row_sequence(const int64_t *offsets, int batch, int64_t row) {
-  int lo = 0, hi = batch;  // offsets[lo] <= row < offsets[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid] <= row) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-__global__ void page_slots_kernel(ExtendArgs a) {
-  const int64_t end = a.offsets[a.batch];
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < a.n_slots; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / a.heads;
-    const int h = (int)(i - row * a.heads);
-    int64_t slot = -1;
-    if (row < end) {
-      const int b = row_sequence(a.offsets, a.batch, row);
-      const int add = a.granted[b];
-      if (add > 0) {
-        const int pos = a.lens_out[b] - add + (int)(row - a.offsets[b]);
-        const int e = a.table[(int64_t)b * a.max_blocks + pos / a.bs];
-        if (e >= 0 && e < a.n_blocks) slot = ((int64_t)e * a.heads + h) * a.bs + pos % a.bs;
-      }
+  if (SLOTS)  // behind the last sequence
+    for (int64_t i = max(lo, rows0) * a.heads + threadIdx.x; i < hi * a.heads; i += kExtendThreads) a.slots[i] = -1;
+  if (STATE) {
+    int64_t total;
+    block_scan(taken, total);
+    if (threadIdx.x == 0) {
+      a.offsets[a.batch] = rows0;
+      *a.free_head_out = (int32_t)(head + total);
     }
-    a.slots[i] = slot;
   }
 }
+
+// Slots up to which one block does the whole call.
+constexpr int64_t kExtendOneBlock = 16384;
 
 struct AppendArgs {
   int batch, heads, bs, max_blocks, d;
-  int64_t n_blocks, n_rows, ld;
+  int64_t n_blocks, n_rows, ld, units;
   const int32_t *table, *lens, *granted;
   const int64_t *offsets;
   const void *k, *v;
   void *kc, *vc, *bounds;
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// One block = one KV head of one touched cache block, a thread per channel.  Work unit u of
-// sequence b: u - (offsets[b] / bs + 2 b) is the touched block's number; a sequence of n rows touches
-// at most n / bs + 2 blocks, so units of different sequences never meet (a few stay empty).
+// Channel minimum and maximum of 16-byte chunks, exact in the rows' own type.
 template <typename T>
-__global__ void append_kv_kernel(AppendArgs a) {
-  const int64_t u = blockIdx.x;
-  const int h = blockIdx.y;
+__device__ __forceinline__ void widen(uint4 &mn, uint4 &mx, const uint4 &v);
+template <>
+__device__ __forceinline__ void widen<float>(uint4 &mn, uint4 &mx, const uint4 &v) {
+  const float *x = reinterpret_cast<const float *>(&v);
+  float *l = reinterpret_cast<float *>(&mn), *u = reinterpret_cast<float *>(&mx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    l[i] = fminf(l[i], x[i]);
+    u[i] = fmaxf(u[i], x[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void widen<__nv_bfloat16>(uint4 &mn, uint4 &mx, const uint4 &v) {
+  const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162 *>(&v);
+  __nv_bfloat162 *l = reinterpret_cast<__nv_bfloat162 *>(&mn), *u = reinterpret_cast<__nv_bfloat162 *>(&mx);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    l[i] = __hmin2(l[i], x[i]);
+    u[i] = __hmax2(u[i], x[i]);
+  }
+}
+__device__ __forceinline__ uint4 shfl4(const uint4 &v, int src) {
+  return make_uint4(__shfl_sync(TQ_FULL_MASK, v.x, src), __shfl_sync(TQ_FULL_MASK, v.y, src), __shfl_sync(TQ_FULL_MASK, v.z, src),
+                    __shfl_sync(TQ_FULL_MASK, v.w, src));
+}
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) { return __ldcs(p); }
+
+constexpr int kAppendWarps = 8, kAppendAhead = 4;
+
+// A copy with a reduction riding along: bound by HBM (4 rows of d in and out per (token, head), and two per
+// block).  A warp takes one KV head of one touched block, whose rows lie together in the cache; the
+// block's warps take neighbouring heads, whose rows lie together in the input.  Lanes hold 16-byte chunks,
+// 32 / chunks rows at a time, kAppendAhead loads of each array in flight.
+//
+// Work unit u of sequence b: u - (offsets[b] / bs + 2 b) is the touched block's number; a sequence of n
+// rows touches at most n / bs + 2 blocks, so units of different sequences never meet (a few stay empty).
+template <typename T>
+__global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = blockIdx.x * (int64_t)kAppendWarps + (threadIdx.x >> 5);
+  const int64_t u = w / a.heads;
+  const int h = (int)(w - u * a.heads);
+  if (u >= a.units) return;
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid] / a.bs + 2 * (int64_t)mid <= u) lo = mid;
+    if (__ldg(a.offsets + mid) / a.bs + 2 * (int64_t)mid <= u) lo = mid;
     else hi = mid;
   }
   const int b = lo;
@@ -189,32 +251,70 @@ __global__ void append_kv_kernel(AppendArgs a) {
   if (j > (len - 1) / a.bs) return;
   const int e = a.table[(int64_t)b * a.max_blocks + j];
   if (e < 0 || e >= a.n_blocks) return;
-  const int64_t t0 = j * a.bs > before ? j * a.bs : before;
-  const int64_t t1 = (j + 1) * a.bs < len ? (j + 1) * a.bs : len;
+  const int64_t begin = j * a.bs;  // the block's first token
+  const int t0 = begin > before ? 0 : (int)(before - begin);
+  const int t1 = begin + a.bs < len ? a.bs : (int)(len - begin);
   const int64_t blk = (int64_t)e * a.heads + h;
-  for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-    T *bound = a.bounds ? static_cast<T *>(a.bounds) + blk * 2 * a.d : nullptr;
-    const bool fresh = j * a.bs >= before;
-    T mn{}, mx{};
-    if (bound && !fresh) {
-      mn = bound[c];
-      mx = bound[a.d + c];
-    }
-    for (int64_t t = t0; t < t1; ++t) {
-      const int64_t src = (row0 + (t - before)) * a.ld + (int64_t)h * a.d + c;
-      const int64_t dst = (blk * a.bs + (t - j * a.bs)) * a.d + c;
-      const T kv = static_cast<const T *>(a.k)[src];
-      if (a.kc) {
-        static_cast<T *>(a.kc)[dst] = kv;
-        static_cast<T *>(a.vc)[dst] = static_cast<const T *>(a.v)[src];
+  const int chunks = a.d * (int)sizeof(T) / 16;
+  const int64_t ld = a.ld * (int64_t)sizeof(T) / 16;
+  const uint4 *k = reinterpret_cast<const uint4 *>(a.k) + (row0 - before + begin) * ld + (int64_t)h * chunks;
+  const uint4 *v = reinterpret_cast<const uint4 *>(a.v) + (row0 - before + begin) * ld + (int64_t)h * chunks;
+  uint4 *kc = reinterpret_cast<uint4 *>(a.kc) + blk * a.bs * chunks, *vc = reinterpret_cast<uint4 *>(a.vc) + blk * a.bs * chunks;
+  uint4 *bound = reinterpret_cast<uint4 *>(a.bounds) + blk * 2 * chunks;
+  const int at_once = chunks < 32 ? 32 / chunks : 1;  // rows per pass
+  const int sub = chunks < 32 ? lane / chunks : 0;
+  for (int c0 = 0; c0 < chunks; c0 += 32) {
+    const int c = chunks < 32 ? lane - sub * chunks : c0 + lane;
+    const bool on = c < chunks && sub < at_once;
+    uint4 mn, mx;
+    bool any = false;
+    for (int t = t0 + sub; on && t < t1; t += kAppendAhead * at_once) {
+      uint4 x[kAppendAhead], y[kAppendAhead];
+#pragma unroll
+      for (int i = 0; i < kAppendAhead; ++i) {
+        const int tt = t + i * at_once;
+        if (tt < t1) {
+          x[i] = ld_stream(k + tt * ld + c);
+          if (a.kc) y[i] = ld_stream(v + tt * ld + c);
+        }
       }
-      if (t == t0 && fresh) mn = mx = kv;
-      if (to_f(kv) < to_f(mn)) mn = kv;
-      if (to_f(kv) > to_f(mx)) mx = kv;
+#pragma unroll
+      for (int i = 0; i < kAppendAhead; ++i) {
+        const int tt = t + i * at_once;
+        if (tt < t1) {
+          if (a.kc) {
+            kc[(int64_t)tt * chunks + c] = x[i];
+            vc[(int64_t)tt * chunks + c] = y[i];
+          }
+          if (!any) mn = mx = x[i];
+          any = true;
+          widen<T>(mn, mx, x[i]);
+        }
+      }
     }
-    if (bound) {
+    if (!a.bounds) continue;
+    // the rows of one pass lie `chunks` lanes apart; at most t1 - t0 of them hold anything
+    const int parts = min(at_once, t1 - t0);
+    for (int i = 1; i < parts; ++i) {
+      const int src = (c + i * chunks) & 31;
+      const uint4 l = shfl4(mn, src), m = shfl4(mx, src);
+      uint4 unused = mx;
+      if (sub == 0 && on) {
+        widen<T>(mn, unused, l);
+        unused = mn;
+        widen<T>(unused, mx, m);
+      }
+    }
+    if (sub == 0 && on) {
+      if (t0 > 0) {  // begun before: its bounds are widened
+        const uint4 l = bound[c], m = bound[chunks + c];
+        uint4 unused = mx;
+        widen<T>(mn, unused, l);
+        unused = mn;
+        widen<T>(unused, mx, m);
+      }
       bound[c] = mn;
-      bound[a.d + c] = mx;
+      bound[chunks + c] = mx;
     }
   }
 }
@@ -243,17 +343,25 @@ extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_le
   if (st != TQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ExtendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, n_free, pages->n_blocks,
-               n_slots / pages->n_kv_heads, n_slots, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
-               seq_lens_out, granted, free_head_out, row_offsets, new_slots};
-  tq_prof_begin(TQK_PAGE_EXTEND, s);
-  page_extend_kernel<<<1, kExtendThreads, 0, s>>>(a);
-  tq_prof_end(TQK_PAGE_EXTEND, s);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && n_slots > 0) {
-    const int64_t want = (n_slots + 255) / 256, most = 16 * (int64_t)tq_sm_count();
+               n_slots / pages->n_kv_heads, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
+               seq_lens_out, granted, free_head_out, row_offsets, new_slots, FastDiv(pages->n_kv_heads),
+               FastDiv(pages->block_size)};
+  cudaError_t e;
+  if (n_slots <= kExtendOneBlock) {
+    tq_prof_begin(TQK_PAGE_EXTEND, s);
+    page_extend_kernel<true, true><<<1, kExtendThreads, 0, s>>>(a);
+    tq_prof_end(TQK_PAGE_EXTEND, s);
+    e = cudaGetLastError();
+  } else {
+    const int64_t want = n_slots / 4096 + 1, most = 4 * (int64_t)tq_sm_count();
     tq_prof_begin(TQK_PAGE_SLOTS, s);
-    page_slots_kernel<<<(unsigned)(want < most ? want : most), 256, 0, s>>>(a);
+    page_extend_kernel<true, false><<<(unsigned)(want < most ? want : most), kExtendThreads, 0, s>>>(a);
     tq_prof_end(TQK_PAGE_SLOTS, s);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return tq_cuda_check(e, "page extend launch");
+    tq_prof_begin(TQK_PAGE_EXTEND, s);
+    page_extend_kernel<false, true><<<1, kExtendThreads, 0, s>>>(a);
+    tq_prof_end(TQK_PAGE_EXTEND, s);
     e = cudaGetLastError();
   }
   return tq_cuda_check(e, "page extend launch");
@@ -283,18 +391,18 @@ extern "C" tq_status tq_append_kv(const tq_pages *pages, const int32_t *seq_lens
   if (!tq_aligned(seq_lens, 4) || !tq_aligned(granted, 4) || !tq_aligned(row_offsets, 8))
     return tq_fail(TQ_EINVAL, "int32 arrays must be 4-byte and int64 arrays 8-byte aligned");
   const int64_t units = n_rows / pages->block_size + 2 * (int64_t)pages->batch;
-  if (units > INT32_MAX || pages->n_kv_heads > 65535)
+  if (units > INT32_MAX / pages->n_kv_heads)
     return tq_fail(TQ_EUNSUPPORTED, "n_rows=%lld, n_kv_heads=%d: too many", (long long)n_rows, pages->n_kv_heads);
   DeviceScope dev_scope;
   st = dev_scope.enter(pages->device);
   if (st != TQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AppendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, d, pages->n_blocks, n_rows, ld,
-               pages->block_table, seq_lens, granted, row_offsets, k_new, v_new, k_cache, v_cache, bounds};
-  const dim3 grid((unsigned)units, (unsigned)pages->n_kv_heads);
+               units, pages->block_table, seq_lens, granted, row_offsets, k_new, v_new, k_cache, v_cache, bounds};
+  const unsigned grid = (unsigned)((units * pages->n_kv_heads + kAppendWarps - 1) / kAppendWarps);
   tq_prof_begin(TQK_APPEND_KV, s);
-  if (dtype == TQ_F32) append_kv_kernel<float><<<grid, 128, 0, s>>>(a);
-  else append_kv_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+  if (dtype == TQ_F32) append_kv_kernel<float><<<grid, 32 * kAppendWarps, 0, s>>>(a);
+  else append_kv_kernel<__nv_bfloat16><<<grid, 32 * kAppendWarps, 0, s>>>(a);
   tq_prof_end(TQK_APPEND_KV, s);
   return tq_cuda_check(cudaGetLastError(), "append launch");
 }

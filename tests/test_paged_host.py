@@ -58,7 +58,7 @@ def test_pages_are_checked(lib, call):
                 dict(block_table=None), dict(block_table=P + 2)):
         assert call(lib, pages(lib, **bad)) == EINVAL, bad
         assert b"pages" in lib.LIB.tq_last_error()
-    for big in (dict(batch=1 << 30, n_kv_heads=2), dict(n_blocks=1 << 30), dict(max_blocks=1 << 20, block_size=1 << 11)):
+    for big in (dict(batch=1 << 30, n_kv_heads=2), dict(n_blocks=1 << 30), dict(n_kv_heads=65536, n_blocks=10), dict(max_blocks=1 << 20, block_size=1 << 11)):
         assert call(lib, pages(lib, **big)) == EUNSUPPORTED, big
 
 
