@@ -23,14 +23,19 @@ struct PagedArgs {
   const int32_t *table, *lens;
   const void *q, *k, *v;
   void *out;
+  FastDiv by_bs;
   int4 *owner;   // [workers]: row whose pieces this worker begins, their number (0: none), slots from one to the next
-  float *piece;  // [workers][2][group][d] o, then [group] m, [group] l of each
+  float *piece;  // [workers][2][piece_floats]: [group][d] o, then [group] m, [group] l of each
 };
 
-constexpr float kLog2e = 1.44269504088896340736f;
+// What a row costs a worker beside its steps (its queries, its first loads, the joining of the warps), in
+// steps of the worker: a batch of 7 rows x 4 heads of 1 to 9999 tokens took
+// TODO
+constexpr int kTeamRowCost = 8, kSoloRowCost = 2;
+// Floats of one piece, a multiple of four.
+__host__ __device__ __forceinline__ int piece_floats(int group, int d) { return (group * (d + 2) + 3) & ~3; }
 
-__device__ __forceinline__ void store1(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+constexpr float kLog2e = 1.44269504088896340736f;
 
 // One warp's stream over the steps of one row, and its softmax state.
 //   WIDE   more than 8 query heads.  Otherwise rows 8 .. 15 of the products' left operand carry the
@@ -76,7 +81,11 @@ struct Stream {
       for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
     for (int kg = 0; kg < kKg; ++kg) {
-      if constexpr (!kQInRegs) load_q<T, kH>(qf[0], a.q, row, a.group, a.d, kg, lane);
+      if constexpr (!kQInRegs) {
+        uint4 raw[kH];
+        load_q<T, kH>(raw, a.q, row, a.group, a.d, kg, lane);
+        make_q<T, kH>(qf[0], raw);
+      }
       const auto &f = qf[kQInRegs ? kg : 0];
 #pragma unroll
       for (int t = 0; t < kT; ++t) {
@@ -215,12 +224,28 @@ struct Stream {
     }
   }
 
-  // Channel of accumulator (tile n, column i of this lane).
-  static __device__ __forceinline__ int channel(int n, int i, int lane) {
-    return kBf ? 8 * n + 2 * (lane & 3) + i : 32 * (n >> 2) + 8 * (lane & 3) + 4 * i + (n & 3);
-  }
   __device__ __forceinline__ float value(int n, int i, int x) const {
     return WIDE ? o[n][2 * x + i] : o[n][i] + o[n][2 + i];
+  }
+  // o of head lane / 4 + 8 x, times f, to d channels at dst.  A lane's columns 2 c, 2 c + 1 of tile n are
+  // channels 8 n + 2 c, 8 n + 2 c + 1 (bf16), or, of four tiles, the eight from 32 (n / 4) + 8 c on (fp32).
+  template <typename O>
+  __device__ __forceinline__ void emit(O *dst, int x, float f, int d, int lane) const {
+    const int c = lane & 3;
+    if constexpr (kBf) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+        if (8 * n < d) store2(dst + 8 * n + 2 * c, value(n, 0, x) * f, value(n, 1, x) * f);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kNt; n += 4)
+        if (8 * n + 8 * c < d) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4 *>(dst + 8 * n + 8 * c + 4 * i) =
+                make_float4(value(n, i, x) * f, value(n + 1, i, x) * f, value(n + 2, i, x) * f, value(n + 3, i, x) * f);
+        }
+    }
   }
 };
 
@@ -229,27 +254,24 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
   using S = Shape<T, D>;
   using St = Stream<T, D, WIDE, PARTS>;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t at_pos[kWarps];
-  __shared__ int at_seq[kWarps];
+  __shared__ Place place[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
   __shared__ float mm[kWarps][16], ll[kWarps][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   StepScan scan;
   scan.run(a.lens, a.batch, a.heads, a.max_len, S::kTok);
-  const int64_t total = scan.total;
   // ---- workers
   const int64_t rows = (int64_t)a.batch * a.heads;
-  const bool solo = rows >= (int64_t)gridDim.x && total < 8 * rows;
-  const int team = solo ? 1 : kWarps;
-  int64_t workers = solo ? (int64_t)gridDim.x * kWarps : (int64_t)gridDim.x;
-  workers = max((int64_t)1, min(workers, total / (solo ? 1 : kWarps)));
+  const bool solo = rows >= (int64_t)gridDim.x && scan.total < 8 * rows;
+  const int team = solo ? 1 : kWarps, extra = solo ? kSoloRowCost : kTeamRowCost;
+  const int64_t workers = max((int64_t)1, min((int64_t)gridDim.x * (solo ? kWarps : 1), scan.total / (solo ? 1 : kWarps)));
+  const Deal deal(scan.total + rows * extra, workers);
   for (int w = 0; w < kWarps; w += team) {
     const int64_t id = solo ? (int64_t)blockIdx.x * kWarps + w : (int64_t)blockIdx.x;
-    if (id < workers) {
-      scan.find(total * id / workers, a.lens, a.max_len, S::kTok, at_seq[w], at_pos[w]);
-    }
+    if (id < workers) find_unit(scan, deal.begin(id), extra, a.lens, a.max_len, S::kTok, place[w]);
   }
   if (lane == 0) a.owner[blockIdx.x * kWarps + warp] = make_int4(0, 0, 0, 0);
   __syncthreads();
@@ -257,14 +279,15 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
   const int slot0 = blockIdx.x * kWarps + lead;
   const int64_t id = solo ? (int64_t)slot0 : (int64_t)blockIdx.x;
   if (id >= workers) return;
-  const int64_t begin = total * id / workers, end = total * (id + 1) / workers;
-  int b = at_seq[lead], len, steps;
-  auto enter = [&](int seq) {
-    len = min(max(a.lens[seq], 0), a.max_len);
+  const int64_t begin = deal.begin(id), end = deal.begin(id + 1);
+  int b = place[lead].seq, len, steps;
+  auto enter = [&](int tokens) {
+    len = min(max(tokens, 0), a.max_len);
     steps = row_steps(len, a.max_len, S::kTok);
   };
-  enter(b);
-  int h = (int)(at_pos[lead] / steps), first = (int)(at_pos[lead] - (int64_t)h * steps);
+  enter(place[lead].len);
+  int h = (int)div64(place[lead].unit, steps + extra);
+  int64_t unit = place[lead].unit - (int64_t)h * (steps + extra);  // place in the row, its cost in front
 
   const unsigned ring = smem_addr(smem) + warp * S::kRing;
   const int esz_row = a.d * (int)sizeof(T);  // bytes of a row in the cache
@@ -275,21 +298,34 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
   St st;
 
   for (int64_t pos = begin; pos < end;) {
-    const int count = (int)min((int64_t)(steps - first), end - pos);
+    const int64_t span = min(steps + extra - unit, end - pos);
+    const int first = (int)max(unit - extra, (int64_t)0), count = (int)max(unit + span - extra, (int64_t)0) - first;
+    auto go_on = [&]() {
+      pos += span;
+      unit = 0;
+      if (pos < end && ++h == a.heads) {
+        h = 0;
+        enter(a.lens[++b]);
+      }
+    };
+    if (count == 0) {  // the worker's run ends in front of the row's first step
+      go_on();
+      continue;
+    }
     const int64_t row = (int64_t)b * a.heads + h;
     const int32_t *table = a.table + (int64_t)b * a.max_blocks;
     const int n = (count - rank + team - 1) / team;
     // block of this lane's token (of the whole step where it lies in one block)
     auto entry = [&](int i) {
       const int t = (first + rank + i * team) * S::kTok + (whole ? 0 : (lane & (S::kTok - 1)));
-      return i < n && t < len ? __ldg(table + t / a.bs) : -1;
+      return i < n && t < len ? __ldg(table + a.by_bs(t)) : -1;
     };
     auto issue = [&](int i, int e) {
       const int stage = i % S::kStages;
       const int t0 = (first + rank + i * team) * S::kTok;
       const bool ok = e >= 0 && e < a.n_blocks;
       const int t = t0 + (whole ? 0 : (lane & (S::kTok - 1)));
-      const int64_t off = ok ? (((int64_t)e * a.heads + h) * a.bs + t % a.bs) * esz_row : 0;
+      const int64_t off = ok ? (((int64_t)e * a.heads + h) * a.bs + (t - a.by_bs(t) * a.bs)) * esz_row : 0;
       uint32_t valid = __ballot_sync(TQ_FULL_MASK, whole ? ok && t0 + lane < len : ok);
       valid &= (1u << S::kTok) - 1u;
       if (lane == 0) masks[warp][stage] = valid;
@@ -307,6 +343,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
     int e[S::kStages];
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
+    uint4 raw[St::kQ][St::kH];  // asked for before the rows, so that it does not queue behind them
+    if constexpr (St::kQInRegs) {
+#pragma unroll
+      for (int kg = 0; kg < St::kKg; ++kg) load_q<T, St::kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
+    }
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) {
       if (i < n) issue(i, e[i]);
@@ -315,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
     int next = e[S::kStages - 1];
     if constexpr (St::kQInRegs) {
 #pragma unroll
-      for (int kg = 0; kg < St::kKg; ++kg) load_q<T, St::kH>(st.qf[kg], a.q, row, a.group, a.d, kg, lane);
+      for (int kg = 0; kg < St::kKg; ++kg) make_q<T, St::kH>(st.qf[kg], raw[kg]);
     }
     st.clear();
     for (int i = 0; i < n; ++i) {
@@ -339,30 +380,18 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
     // ---- the row's end, or the worker's: the output, or a piece of it
     const bool starts = first == 0, ends = first + count == steps;
     const int g = a.group;
-    float *piece = a.piece + ((int64_t)slot0 * 2 + (starts ? 1 : 0)) * g * (a.d + 2);
+    const bool done = starts && ends;
+    float *piece = a.piece + ((int64_t)slot0 * 2 + (starts ? 1 : 0)) * piece_floats(g, a.d);
+    O *out = static_cast<O *>(a.out) + row * g * a.d;
     if (solo) {
 #pragma unroll
       for (int x = 0; x < St::kH; ++x) {
         const int hd = (lane >> 2) + 8 * x;
         if (hd >= g) continue;
-        if (starts && ends) {
-          const float inv = st.l[x] > 0.f ? 1.f / st.l[x] : 0.f;
-          O *out = static_cast<O *>(a.out) + (row * g + hd) * a.d;
-#pragma unroll
-          for (int t = 0; t < St::kNt; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int c = St::channel(t, i, lane);
-              if (c < a.d) store1(out + c, st.value(t, i, x) * inv);
-            }
+        if (done) {
+          st.emit(out + hd * a.d, x, st.l[x] > 0.f ? 1.f / st.l[x] : 0.f, a.d, lane);
         } else {
-#pragma unroll
-          for (int t = 0; t < St::kNt; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int c = St::channel(t, i, lane);
-              if (c < a.d) piece[hd * a.d + c] = st.value(t, i, x);
-            }
+          st.emit(piece + hd * a.d, x, 1.f, a.d, lane);
           if ((lane & 3) == 0) {
             piece[g * a.d + hd] = st.m[x];
             piece[g * a.d + g + hd] = st.l[x];
@@ -370,38 +399,44 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
         }
       }
     } else {
-      float *buf = reinterpret_cast<float *>(smem) + warp * 16 * D;
+      // padded rows: a warp's stores below touch every bank once
+      constexpr int kPad = D + (St::kBf ? 8 : 4);
+      float *buf = reinterpret_cast<float *>(smem);
       __syncthreads();  // every warp's ring is drained: its shared memory holds the warps' sums now
 #pragma unroll
       for (int x = 0; x < St::kH; ++x) {
         const int hd = (lane >> 2) + 8 * x;
         if (hd >= g) continue;
-#pragma unroll
-        for (int t = 0; t < St::kNt; ++t)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) buf[hd * D + St::channel(t, i, lane)] = st.value(t, i, x);
+        st.emit(buf + (warp * 16 + hd) * kPad, x, 1.f, D, lane);
         if ((lane & 3) == 0) {
           mm[warp][hd] = st.m[x];
           ll[warp][hd] = st.l[x];
         }
       }
       __syncthreads();
-      for (int idx = threadIdx.x; idx < g * D; idx += kThreads) {
-        const int hd = idx / D, c = idx % D;
-        float top = -INFINITY, sum = 0.f, x = 0.f;
+      for (int idx = threadIdx.x; idx < g * (D / 4); idx += kThreads) {
+        const int hd = idx / (D / 4), c = 4 * (idx % (D / 4));
+        if (c >= a.d) continue;
+        float top = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mm[w][hd]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float f = mm[w][hd] == -INFINITY ? 0.f : exp2a(mm[w][hd] - top);
+          const float4 x = *reinterpret_cast<const float4 *>(buf + (w * 16 + hd) * kPad + c);
           sum = fmaf(f, ll[w][hd], sum);
-          x = fmaf(f, reinterpret_cast<const float *>(smem)[(w * 16 + hd) * D + c], x);
+          v.x = fmaf(f, x.x, v.x);
+          v.y = fmaf(f, x.y, v.y);
+          v.z = fmaf(f, x.z, v.z);
+          v.w = fmaf(f, x.w, v.w);
         }
-        if (c >= a.d) continue;
-        if (starts && ends) {
-          store1(static_cast<O *>(a.out) + (row * g + hd) * a.d + c, sum > 0.f ? x / sum : 0.f);
+        if (done) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          store2(out + hd * a.d + c, v.x * inv, v.y * inv);
+          store2(out + hd * a.d + c + 2, v.z * inv, v.w * inv);
         } else {
-          piece[hd * a.d + c] = x;
+          *reinterpret_cast<float4 *>(piece + hd * a.d + c) = v;
           if (c == 0) {
             piece[g * a.d + hd] = top;
             piece[g * a.d + g + hd] = sum;
@@ -412,71 +447,92 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
     }
     if (starts && !ends && rank == 0 && lane == 0) {
       // the row's last step decides how many workers hold pieces of it
-      const int64_t last = pos + steps - 1;
-      int64_t to = last * workers / total;
-      while (total * (to + 1) / workers <= last) ++to;
-      while (total * to / workers > last) --to;
+      const int64_t to = deal.owner(pos - unit + extra + steps - 1);
       a.owner[slot0] = make_int4((int)row, (int)(to - id + 1), solo ? 1 : kWarps, 0);
     }
-
-    pos += count;
-    first = 0;
-    if (pos < end && ++h == a.heads) {
-      h = 0;
-      enter(++b);
-    }
+    go_on();
   }
 }
 
-// Joins the pieces of rows that several workers shared.  Block (x, head): the rows that block x of the
-// kernel above began; its warps take pieces in turn, lanes four channels each.
-constexpr int kMergeWarps = 8;
+// Joins the pieces of rows that several workers shared: block x, the rows that block x of the kernel above
+// began.  Threads hold four channels of one head each; as many groups of them as the block has room for
+// take pieces in turn.  Latency-bound (a few hundred KB in all): four pieces in flight per thread.
+constexpr int kMergeThreads = 256;
 template <typename O>
-__global__ void __launch_bounds__(32 * kMergeWarps) attend_paged_merge_kernel(PagedArgs a) {
-  __shared__ float sm[kMergeWarps], sl[kMergeWarps];
-  __shared__ __align__(16) float so[kMergeWarps][kPagedMaxD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hd = blockIdx.y, g = a.group;
-  const int64_t stride = (int64_t)g * (a.d + 2);
+__global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(PagedArgs a) {
+  __shared__ float4 so[kMergeThreads];
+  __shared__ float sm[kMergeThreads], sl[kMergeThreads];
+  const int g = a.group, vecs = g * a.d / 4, tid = threadIdx.x;
+  const int groups = vecs < kMergeThreads ? kMergeThreads / vecs : 1;
+  const int64_t stride = piece_floats(g, a.d);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  int4 own[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) own[w] = a.owner[blockIdx.x * kWarps + w];
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
-    const int slot = blockIdx.x * kWarps + w;
-    const int4 own = a.owner[slot];
-    if (own.y == 0) continue;
-    float m = -INFINITY, l = 0.f, o[kPagedMaxD / 32];
+    const int n = own[w].y;
+    if (n == 0) continue;
+    const float *base = a.piece + (int64_t)(blockIdx.x * kWarps + w) * 2 * stride;
+    for (int v0 = 0; v0 < vecs; v0 += kMergeThreads) {
+      const int grp = vecs < kMergeThreads ? tid / vecs : 0, v = v0 + tid - grp * vecs;
+      const bool on = grp < groups && v < vecs;
+      const int hd = on ? 4 * v / a.d : 0;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p0 = grp; on && p0 < n; p0 += 4 * groups) {
+        float pm[4], pl[4];
+        float4 po[4];
 #pragma unroll
-    for (int i = 0; i < kPagedMaxD / 32; ++i) o[i] = 0.f;
-    for (int p = warp; p < own.y; p += kMergeWarps) {
-      const float *piece = a.piece + ((int64_t)(slot + p * own.z) * 2 + (p == 0 ? 1 : 0)) * stride;
-      const float pm = piece[g * a.d + hd], pl = piece[g * a.d + g + hd];
-      const float to = fmaxf(m, pm);
-      if (to == -INFINITY) continue;
-      const float f0 = exp2a(m - to), f1 = exp2a(pm - to);
-      m = to;
-      l = l * f0 + pl * f1;
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * groups;
+          pm[i] = -INFINITY;
+          if (p < n) {
+            const float *piece = base + ((int64_t)p * own[w].z * 2 + (p == 0 ? 1 : 0)) * stride;
+            pm[i] = piece[g * a.d + hd];
+            pl[i] = piece[g * a.d + g + hd];
+            po[i] = *reinterpret_cast<const float4 *>(piece + 4 * v);
+          }
+        }
 #pragma unroll
-      for (int i = 0; i < kPagedMaxD / 32; ++i) {
-        const int c = lane + 32 * i;
-        if (c < a.d) o[i] = o[i] * f0 + piece[hd * a.d + c] * f1;
+        for (int i = 0; i < 4; ++i) {
+          if (pm[i] == -INFINITY) continue;
+          const float to = fmaxf(m, pm[i]), f0 = exp2a(m - to), f1 = exp2a(pm[i] - to);
+          m = to;
+          l = l * f0 + pl[i] * f1;
+          o.x = o.x * f0 + po[i].x * f1;
+          o.y = o.y * f0 + po[i].y * f1;
+          o.z = o.z * f0 + po[i].z * f1;
+          o.w = o.w * f0 + po[i].w * f1;
+        }
+      }
+      if (groups > 1) {
+        sm[tid] = m;
+        sl[tid] = l;
+        so[tid] = o;
+        __syncthreads();
+        for (int i = 1; grp == 0 && on && i < groups; ++i) {
+          const float im = sm[tid + i * vecs];
+          if (im == -INFINITY) continue;
+          const float4 io = so[tid + i * vecs];
+          const float to = fmaxf(m, im), f0 = exp2a(m - to), f1 = exp2a(im - to);
+          m = to;
+          l = l * f0 + sl[tid + i * vecs] * f1;
+          o.x = o.x * f0 + io.x * f1;
+          o.y = o.y * f0 + io.y * f1;
+          o.z = o.z * f0 + io.z * f1;
+          o.w = o.w * f0 + io.w * f1;
+        }
+        __syncthreads();
+      }
+      if (grp == 0 && on) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        O *out = static_cast<O *>(a.out) + (int64_t)own[w].x * g * a.d + 4 * v;
+        store2(out, o.x * inv, o.y * inv);
+        store2(out + 2, o.z * inv, o.w * inv);
       }
     }
-    if (lane == 0) {
-      sm[warp] = m;
-      sl[warp] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < kPagedMaxD / 32; ++i) so[warp][lane + 32 * i] = o[i];
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += 32 * kMergeWarps) {
-      float top = -INFINITY, sum = 0.f, x = 0.f;
-      for (int v = 0; v < kMergeWarps; ++v) top = fmaxf(top, sm[v]);
-      for (int v = 0; v < kMergeWarps; ++v) {
-        const float f = sm[v] == -INFINITY ? 0.f : exp2a(sm[v] - top);
-        sum = fmaf(f, sl[v], sum);
-        x = fmaf(f, so[v][c], x);
-      }
-      store1(static_cast<O *>(a.out) + ((int64_t)own.x * g + hd) * a.d + c, sum > 0.f ? x / sum : 0.f);
-    }
-    __syncthreads();
   }
 }
 
@@ -500,13 +556,8 @@ tq_status check_attend(const tq_pages *pages, int32_t max_seq_len, int32_t n_q_h
 // one workspace size serves them.
 int attend_grid(const tq_pages &p, int32_t max_seq_len, int32_t d) {
   const int occ = d <= 64 ? Shape<float, 64>::kOcc : d <= 128 ? Shape<float, 128>::kOcc : Shape<float, 256>::kOcc;
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p.device) != cudaSuccess || sms <= 0) {
-    cudaGetLastError();
-    sms = 148;
-  }
   const int64_t steps = (int64_t)p.batch * p.n_kv_heads * (max_seq_len <= 8 ? 1 : (max_seq_len - 1) / 8 + 1);
-  const int64_t want = (steps + kWarps - 1) / kWarps, most = (int64_t)occ * sms;
+  const int64_t want = (steps + kWarps - 1) / kWarps, most = (int64_t)occ * tq_device_sms(p.device);
   return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -519,27 +570,13 @@ cudaError_t launch(const PagedArgs &a, int grid, cudaStream_t st) {
   cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   tq_prof_begin(TQK_ATTEND_PAGED, st);
-  kern<<<grid, kThreads, S::kSmem, st>>>(a);
+  e = tq_launch_dependent(kern, dim3((unsigned)grid), kThreads, S::kSmem, st, a);
   tq_prof_end(TQK_ATTEND_PAGED, st);
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 mgrid((unsigned)grid, (unsigned)a.group);
-  if (tq_prof_on()) {
-    tq_prof_begin(TQK_ATTEND_PAGED_MERGE, st);
-    attend_paged_merge_kernel<O><<<mgrid, 32 * kMergeWarps, 0, st>>>(a);
-    tq_prof_end(TQK_ATTEND_PAGED_MERGE, st);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = mgrid;
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_paged_merge_kernel<O>, a);
+  tq_prof_begin(TQK_ATTEND_PAGED_MERGE, st);
+  e = tq_launch_dependent(attend_paged_merge_kernel<O>, dim3((unsigned)grid), kMergeThreads, 0, st, a);
+  tq_prof_end(TQK_ATTEND_PAGED_MERGE, st);
+  return e;
 }
 
 template <typename T, int PARTS, typename O>
@@ -558,7 +595,7 @@ extern "C" tq_status tq_attend_paged_workspace_size(const tq_pages *pages, int32
   if (st != TQ_OK) return st;
   if (!bytes) return tq_fail(TQ_EINVAL, "bytes is NULL");
   const int grid = attend_grid(*pages, max_seq_len, d);
-  *bytes = owner_bytes(grid) + sizeof(float) * 2 * (size_t)grid * kWarps * (n_q_heads / pages->n_kv_heads) * (d + 2);
+  *bytes = owner_bytes(grid) + sizeof(float) * 2 * (size_t)grid * kWarps * piece_floats(n_q_heads / pages->n_kv_heads, d);
   return TQ_OK;
 }
 
@@ -587,7 +624,7 @@ extern "C" tq_status tq_attend_paged(const tq_pages *pages, const int32_t *seq_l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PagedArgs a{pages->batch, pages->n_kv_heads, n_q_heads / pages->n_kv_heads, pages->block_size, pages->max_blocks,
               max_seq_len, d, pages->n_blocks, scale != 0.f ? scale : 1.f / sqrtf((float)d), pages->block_table, seq_lens,
-              q, k_cache, v_cache, out, nullptr, nullptr};
+              q, k_cache, v_cache, out, FastDiv(pages->block_size), nullptr, nullptr};
   const int grid = attend_grid(*pages, max_seq_len, d);
   a.owner = static_cast<int4 *>(ws);
   a.piece = reinterpret_cast<float *>(static_cast<char *>(ws) + owner_bytes(grid));

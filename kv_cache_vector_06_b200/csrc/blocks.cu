@@ -13,6 +13,9 @@ struct BlockScoreArgs {
   float *out;
 };
 
+// Steps that a row costs a warp beside its own: its queries and its first loads.
+constexpr int kRowCost = 2;
+
 // max_c over a box: max(q_c lower_c, q_c upper_c) = min(q_c, 0) lower_c + max(q_c, 0) upper_c, so the
 // scores of a step's blocks are two products over d, one with each half of the query.  Bound: 2 d values
 // per block, read once for the whole group: HBM.  The loads, the operands' layout and the division of the
@@ -24,31 +27,35 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
   constexpr int kH = WIDE ? 2 : 1, kParts = kBf ? 1 : 2, kKg = S::kCh / 4, kT = S::kTok / 8;
   constexpr bool kQInRegs = kKg * kH * kParts * 4 <= 64;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t at_pos[kWarps];
-  __shared__ int at_seq[kWarps];
+  __shared__ Place place[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, r = lane >> 2;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   StepScan scan;
   scan.run(a.lens, a.batch, a.heads, a.max_len, a.step_tokens);
-  const int64_t total = scan.total, workers = min((int64_t)gridDim.x * kWarps, total);
+  const int64_t workers = min((int64_t)gridDim.x * kWarps, scan.total);
+  const Deal deal(scan.total + (int64_t)a.batch * a.heads * kRowCost, workers);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const int64_t id = (int64_t)blockIdx.x * kWarps + w;
-    if (id < workers) scan.find(total * id / workers, a.lens, a.max_len, a.step_tokens, at_seq[w], at_pos[w]);
+    if (id < workers) find_unit(scan, deal.begin(id), kRowCost, a.lens, a.max_len, a.step_tokens, place[w]);
   }
   __syncthreads();
   const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
   if (id >= workers) return;
-  const int64_t begin = total * id / workers, end = total * (id + 1) / workers;
-  int b = at_seq[warp], steps = row_steps(a.lens[b], a.max_len, a.step_tokens);
-  int held = held_blocks(a.lens[b], a.bs, a.max_blocks);
-  int h = (int)(at_pos[warp] / steps), first = (int)(at_pos[warp] - (int64_t)h * steps);
+  const int64_t begin = deal.begin(id), end = deal.begin(id + 1);
+  int b = place[warp].seq, steps = row_steps(place[warp].len, a.max_len, a.step_tokens);
+  int held = held_blocks(place[warp].len, a.bs, a.max_blocks);
+  int h = (int)div64(place[warp].unit, steps + kRowCost);
+  int64_t unit = place[warp].unit - (int64_t)h * (steps + kRowCost);  // place in the row, its cost in front
   const unsigned ring = smem_addr(smem) + warp * S::kRing;
   const int row_bytes = a.d * (int)sizeof(T), dch = row_bytes / 16;
 
   for (int64_t pos = begin; pos < end;) {
-    const int n = (int)min((int64_t)(steps - first), end - pos);
+    const int64_t span = min(steps + kRowCost - unit, end - pos);
+    const int first = (int)max(unit - kRowCost, (int64_t)0), n = (int)max(unit + span - kRowCost, (int64_t)0) - first;
     const int64_t row = (int64_t)b * a.heads + h;
     const int32_t *table = a.table + (int64_t)b * a.max_blocks;
     auto entry = [&](int i) {
@@ -75,6 +82,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
     int e[S::kStages];
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
+    uint4 raw[kQInRegs ? kKg : 1][kH];  // asked for before the bounds, so that it does not queue behind them
+    if constexpr (kQInRegs) {
+#pragma unroll
+      for (int kg = 0; kg < kKg; ++kg) load_q<T, kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
+    }
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) {
       if (i < n) issue(i, e[i]);
@@ -84,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
     uint32_t qf[kQInRegs ? kKg : 1][kH][kParts][4];
     if constexpr (kQInRegs) {
 #pragma unroll
-      for (int kg = 0; kg < kKg; ++kg) load_q<T, kH>(qf[kg], a.q, row, a.group, a.d, kg, lane);
+      for (int kg = 0; kg < kKg; ++kg) make_q<T, kH>(qf[kg], raw[kg]);
     }
     for (int i = 0; i < n; ++i) {
       cp_wait<S::kStages - 2>();
@@ -102,7 +114,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
         for (int x = 0; x < 4; ++x) s[t][x] = 0.f;
 #pragma unroll
       for (int kg = 0; kg < kKg; ++kg) {
-        if constexpr (!kQInRegs) load_q<T, kH>(qf[0], a.q, row, a.group, a.d, kg, lane);
+        if constexpr (!kQInRegs) {
+          load_q<T, kH>(raw[0], a.q, row, a.group, a.d, kg, lane);
+          make_q<T, kH>(qf[0], raw[0]);
+        }
         const auto &f = qf[kQInRegs ? kg : 0];
 #pragma unroll
         for (int up = 0; up < 2; ++up) {
@@ -166,10 +181,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
     }
     cp_wait<0>();
     __syncwarp();
-    if (first + n == steps)  // behind the row's last step
+    if (n > 0 && first + n == steps)  // behind the row's last step
       for (int64_t j = (int64_t)steps * S::kTok + lane; j < a.max_blocks; j += 32) a.out[row * a.max_blocks + j] = -INFINITY;
-    pos += n;
-    first = 0;
+    pos += span;
+    unit = 0;
     if (pos < end && ++h == a.heads) {
       h = 0;
       ++b;
@@ -180,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
 }
 
 template <typename T, int D>
-cudaError_t launch_scores_d(BlockScoreArgs a, cudaStream_t st) {
+cudaError_t launch_scores_d(BlockScoreArgs a, int device, cudaStream_t st) {
   using S = Shape<T, D>;
   const int64_t step = (int64_t)S::kTok * a.bs;
   a.step_tokens = (int)(step < INT32_MAX ? step : INT32_MAX);
@@ -189,11 +204,11 @@ cudaError_t launch_scores_d(BlockScoreArgs a, cudaStream_t st) {
   cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t want = ((int64_t)a.batch * a.heads * ((a.max_blocks - 1) / S::kTok + 1) + kWarps - 1) / kWarps;
-  const int64_t most = (int64_t)S::kOcc * tq_sm_count();
+  const int64_t most = (int64_t)S::kOcc * tq_device_sms(device);
   tq_prof_begin(TQK_BLOCK_SCORES, st);
-  kern<<<(unsigned)(want < most ? want : most), kThreads, S::kSmem, st>>>(a);
+  e = tq_launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), kThreads, S::kSmem, st, a);
   tq_prof_end(TQK_BLOCK_SCORES, st);
-  return cudaGetLastError();
+  return e;
 }
 
 struct SelectArgs {
@@ -252,8 +267,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
   __shared__ int hist[256];
   __shared__ uint32_t found;
   __shared__ int left;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
-  const int b = (int)(row / a.heads), h = (int)(row - (int64_t)b * a.heads);
+  const int b = (int)(blockIdx.x / (unsigned)a.heads), h = (int)(blockIdx.x - (unsigned)b * (unsigned)a.heads);
   const int len0 = a.lens[b];
   const int n = held_blocks(len0, a.bs, a.max_blocks);
   const int64_t most = (int64_t)n * a.bs;
@@ -390,11 +407,11 @@ extern "C" tq_status tq_block_scores(const tq_pages *pages, const int32_t *seq_l
                    d, 0, 0, pages->n_blocks, pages->block_table, seq_lens, q, bounds, scores};
   cudaError_t e;
   if (dtype == TQ_F32)
-    e = d <= 64 ? launch_scores_d<float, 64>(a, s) : d <= 128 ? launch_scores_d<float, 128>(a, s) : launch_scores_d<float, 256>(a, s);
+    e = d <= 64 ? launch_scores_d<float, 64>(a, pages->device, s) : d <= 128 ? launch_scores_d<float, 128>(a, pages->device, s) : launch_scores_d<float, 256>(a, pages->device, s);
   else
-    e = d <= 64    ? launch_scores_d<__nv_bfloat16, 64>(a, s)
-        : d <= 128 ? launch_scores_d<__nv_bfloat16, 128>(a, s)
-                   : launch_scores_d<__nv_bfloat16, 256>(a, s);
+    e = d <= 64    ? launch_scores_d<__nv_bfloat16, 64>(a, pages->device, s)
+        : d <= 128 ? launch_scores_d<__nv_bfloat16, 128>(a, pages->device, s)
+                   : launch_scores_d<__nv_bfloat16, 256>(a, pages->device, s);
   return tq_cuda_check(e, "block scores launch");
 }
 
@@ -422,8 +439,8 @@ extern "C" tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_
                pages->n_blocks, pages->block_table, seq_lens, scores, sel_table, sel_lens};
   tq_prof_begin(TQK_SELECT_BLOCKS, s);
   const unsigned grid = (unsigned)(pages->batch * pages->n_kv_heads);
-  if (pages->max_blocks <= 4 * kSelectThreads) select_blocks_kernel<4><<<grid, kSelectThreads, 0, s>>>(a);
-  else select_blocks_kernel<16><<<grid, kSelectThreads, 0, s>>>(a);
+  const cudaError_t e = tq_launch_dependent(pages->max_blocks <= 4 * kSelectThreads ? select_blocks_kernel<4> : select_blocks_kernel<16>,
+                                            dim3(grid), kSelectThreads, 0, s, a);
   tq_prof_end(TQK_SELECT_BLOCKS, s);
-  return tq_cuda_check(cudaGetLastError(), "block selection launch");
+  return tq_cuda_check(e, "block selection launch");
 }

@@ -89,24 +89,53 @@ __device__ __forceinline__ int value_chunk(int row, int ch) {
 }
 
 // Chunk 4 kg + lane % 4 of query head lane / 4 (+ 8 x) of row `row`: this lane's part of the left operand, the
-// channels in the order in which a key's chunk holds them.  fp32: split into TF32 parts.
+// channels in the order in which a key's chunk holds them.
 template <typename T, int H>
-__device__ __forceinline__ void load_q(uint32_t (&f)[H][sizeof(T) == 2 ? 1 : 2][4], const void *q, int64_t row, int group, int d, int kg,
-                                       int lane) {
+__device__ __forceinline__ void load_q(uint4 (&v)[H], const void *q, int64_t row, int group, int d, int kg, int lane) {
   const int ch = 4 * kg + (lane & 3);
 #pragma unroll
   for (int x = 0; x < H; ++x) {
     const int hd = (lane >> 2) + 8 * x;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    v[x] = make_uint4(0u, 0u, 0u, 0u);
     if (hd < group && ch < d * (int)sizeof(T) / 16)
-      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(q) + (row * group + hd) * d) + ch);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      v[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(q) + (row * group + hd) * d) + ch);
+  }
+}
+// The operand itself; fp32: split into TF32 parts.
+template <typename T, int H>
+__device__ __forceinline__ void make_q(uint32_t (&f)[H][sizeof(T) == 2 ? 1 : 2][4], const uint4 (&v)[H]) {
+#pragma unroll
+  for (int x = 0; x < H; ++x) {
+    const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(T) == 2) f[x][0][i] = w[i];
       else split_tf32(w[i], f[x][0][i], f[x][1][i]);
     }
   }
+}
+
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
+
+// Launch that may begin while the kernel before it on the stream ends: every kernel launched so waits for
+// that one with griddepcontrol.wait before it touches memory, and lets its own successor begin at once.
+// With per-kernel profiling on, an event sits between the two and a plain launch is used.
+template <typename... P, typename... A>
+cudaError_t tq_launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = tq_prof_on() ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1: q = (mulhi(n, mul) + n) >> shift with
@@ -131,10 +160,28 @@ __device__ __forceinline__ int row_steps(int len, int max_len, int tok) {
   return len <= tok ? 1 : (len - 1) / tok + 1;
 }
 
+// a / b for 0 <= a, 0 < b: the 32-bit division where it will do (the 64-bit one takes some 100 instructions).
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+// `total` units dealt to `workers` in equal runs, the first `total % workers` of them one longer.
+struct Deal {
+  int64_t each, more;
+  __device__ __forceinline__ Deal(int64_t total, int64_t workers) : each(div64(total, workers)), more(total - each * workers) {}
+  __device__ __forceinline__ int64_t begin(int64_t id) const { return each * id + min(id, more); }
+  __device__ __forceinline__ int64_t owner(int64_t unit) const {
+    const int64_t longer = (each + 1) * more;  // units of the longer runs
+    return unit < longer ? div64(unit, each + 1) : more + div64(unit - longer, each);
+  }
+};
+
 // The steps of all (sequence, KV head) rows laid end to end, sequence by sequence: each thread of the
-// block sums a run of sequences, then a block scan.  kThreads threads; ends with a block barrier.
+// block sums a run of sequences, then a block scan.  kThreads threads; has one block barrier.
 struct StepScan {
-  int64_t b0, b1;       // this thread's sequences
+  int b0, b1;           // this thread's sequences
+  int len0;             // the first one's length
   int64_t before, mine; // steps before and in them
   int64_t total;
   int heads;
@@ -143,10 +190,11 @@ struct StepScan {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (batch + kThreads - 1) / kThreads;
     heads = n_heads;
-    b0 = min((int64_t)threadIdx.x * per, (int64_t)batch);
-    b1 = min(b0 + per, (int64_t)batch);
-    mine = 0;
-    for (int64_t b = b0; b < b1; ++b) mine += row_steps(lens[b], max_len, tok);
+    b0 = (int)min((int64_t)threadIdx.x * per, (int64_t)batch);
+    b1 = (int)min((int64_t)b0 + per, (int64_t)batch);
+    len0 = b0 < b1 ? lens[b0] : 0;
+    mine = b0 < b1 ? row_steps(len0, max_len, tok) : 0;
+    for (int b = b0 + 1; b < b1; ++b) mine += row_steps(lens[b], max_len, tok);
     mine *= heads;
     int64_t incl = mine;
 #pragma unroll
@@ -160,23 +208,34 @@ struct StepScan {
     before = incl - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
+      const int64_t x = wsum[w];
+      if (w < warp) before += x;
+      total += x;
     }
-  }
-  // The thread that holds step `pos` writes its sequence and the step's place in the sequence's rows.
-  __device__ __forceinline__ void find(int64_t pos, const int32_t *lens, int max_len, int tok, int &seq, int64_t &place) const {
-    if (pos < before || pos >= before + mine) return;
-    int64_t left = pos - before, b = b0;
-    for (;; ++b) {
-      const int64_t n = (int64_t)row_steps(lens[b], max_len, tok) * heads;
-      if (left < n) break;
-      left -= n;
-    }
-    seq = (int)b;
-    place = left;
   }
 };
+
+// Where a worker begins: a sequence, its length, and a unit's place in the sequence's rows.
+struct Place {
+  int seq, len;
+  int64_t unit;
+};
+
+// With `extra` units of work counted in front of every row's steps (what a row costs beside them): the
+// thread that holds unit `pos` of all rows writes where it lies.
+__device__ __forceinline__ void find_unit(const StepScan &s, int64_t pos, int extra, const int32_t *lens, int max_len, int tok, Place &out) {
+  const int64_t front = s.before + (int64_t)s.b0 * s.heads * extra;
+  int64_t left = pos - front;
+  if (left < 0 || left >= s.mine + (int64_t)(s.b1 - s.b0) * s.heads * extra) return;
+  int b = s.b0, len = s.len0;
+  for (;;) {
+    const int64_t n = (int64_t)(extra + row_steps(len, max_len, tok)) * s.heads;
+    if (left < n) break;
+    left -= n;
+    len = lens[++b];
+  }
+  out = Place{b, len, left};
+}
 
 // Blocks that hold a sequence's tokens: ceil(len / bs), with the length clamped to the table.
 __device__ __forceinline__ int held_blocks(int len, int bs, int max_blocks) {

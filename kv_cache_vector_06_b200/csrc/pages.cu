@@ -1,7 +1,22 @@
 // Paged-cache bookkeeping: block tables, lengths and slot maps from request lengths
 // (tq_page_extend), and the append of uncompressed rows with the channel bounds of every block's
 // keys (tq_append_kv).
+#include <atomic>
+
 #include "paged_device.cuh"
+
+int tq_device_sms(int device) {
+  constexpr int kMax = 64;
+  static std::atomic<int> known[kMax];
+  if (device >= 0 && device < kMax && known[device].load(std::memory_order_relaxed) > 0) return known[device];
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (device >= 0 && device < kMax) known[device] = n;
+  return n;
+}
 
 tq_status tq_check_pages(const tq_pages *p) {
   tq_fail(TQ_OK, "%s", "");
@@ -69,7 +84,7 @@ struct ExtendArgs {
   const int32_t *lens, *grow, *free_blocks, *free_head;
   int32_t *lens_out, *granted, *free_head_out;
   int64_t *offsets, *slots;
-  FastDiv by_heads, by_bs;
+  FastDiv by_parts, by_bs;  // heads / VEC, block_size
 };
 
 // What one sequence of the current chunk needs for its slots.
@@ -88,15 +103,18 @@ struct Grown {
 // sequence take one block that does both halves; for whole prompts every block of a large grid repeats
 // the scan (a microsecond) and writes its share, 8 bytes per (row, head), and STATE, the lengths and
 // counters, follows in a second launch: they may be updated in place, after every block has read them.
-template <bool SLOTS, bool STATE>
+//
+// A thread writes the slots of VEC neighbouring heads of a row at once, which differ by a block's tokens:
+// the row's look-ups, some 60 instructions, are what bounds this kernel before the stores do.
+template <bool SLOTS, bool STATE, int VEC>
 __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs a) {
   __shared__ int64_t first_row[kExtendThreads + 1];
   __shared__ Grown grown[kExtendThreads];
   int64_t rows0 = 0, need0 = 0;  // sums before this chunk
   int64_t taken = 0;             // blocks granted, this thread's sequences
   const int64_t most = (int64_t)a.max_blocks * a.bs;
-  if (!SLOTS) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  else asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t head = min(max((int64_t)*a.free_head, (int64_t)0), (int64_t)a.n_free);
   const int64_t lo = a.n_rows * blockIdx.x / gridDim.x, hi = a.n_rows * (blockIdx.x + 1) / gridDim.x;
   for (int b0 = 0; b0 < a.batch; b0 += kExtendThreads) {
@@ -125,14 +143,15 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
       grown[threadIdx.x] = Grown{(int)len, (int)have, (int)(ok ? head + upto : 0), ok && add > 0};
       __syncthreads();
       const int64_t r0 = max(lo, rows0), r1 = min(hi, rows0 + rows_total);
-      // (rows of a block) x heads stays below 2^31 in a pass of this many rows
-      const int64_t pass = max((int64_t)1, (int64_t)(1 << 30) / a.heads);
+      // rows x heads stays below 2^31 in a pass of this many rows
+      const int parts = a.heads / VEC;
+      const int64_t pass = max((int64_t)1, (int64_t)(1 << 30) / parts);
       for (int64_t p0 = r0; p0 < r1; p0 += pass) {
-        const int n = (int)(min(r1, p0 + pass) - p0) * a.heads;
+        const int n = (int)(min(r1, p0 + pass) - p0) * parts;
         int s = 0;  // sequence of the last row looked up: rows come in order
         int64_t s_lo = 1, s_hi = 0;
         for (int i = threadIdx.x; i < n; i += kExtendThreads) {
-          const int k = a.by_heads(i), h = i - k * a.heads;
+          const int k = a.by_parts(i), h = (i - k * parts) * VEC;
           const int64_t r = p0 + k;
           if (r < s_lo || r >= s_hi) {
             int u = 0, v = count;  // first_row[u] <= r < first_row[v]
@@ -159,7 +178,14 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
             }
             if (e >= 0 && e < a.n_blocks) slot = ((int64_t)e * a.heads + h) * a.bs + off;
           }
-          a.slots[p0 * a.heads + i] = slot;
+          const int64_t step = slot < 0 ? 0 : a.bs;
+          if constexpr (VEC == 1) {
+            a.slots[p0 * parts + i] = slot;
+          } else {
+            longlong2 *to = reinterpret_cast<longlong2 *>(a.slots) + (p0 * parts + i) * (VEC / 2);
+#pragma unroll
+            for (int x = 0; x < VEC / 2; ++x) to[x] = make_longlong2(slot + 2 * x * step, slot + (2 * x + 1) * step);
+          }
         }
       }
       __syncthreads();
@@ -179,8 +205,8 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
   }
 }
 
-// Slots up to which one block does the whole call.
-constexpr int64_t kExtendOneBlock = 16384;
+// Slots, in units of VEC, up to which one block does the whole call.
+constexpr int64_t kExtendOneBlock = 4096;
 
 struct AppendArgs {
   int batch, heads, bs, max_blocks, d;
@@ -231,6 +257,8 @@ constexpr int kAppendWarps = 8, kAppendAhead = 4;
 // rows touches at most n / bs + 2 blocks, so units of different sequences never meet (a few stay empty).
 template <typename T>
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t w = blockIdx.x * (int64_t)kAppendWarps + (threadIdx.x >> 5);
   const int64_t u = w / a.heads;
@@ -319,6 +347,25 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   }
 }
 
+template <int VEC>
+cudaError_t launch_extend(const ExtendArgs &a, int64_t n_slots, int device, cudaStream_t st) {
+  if (n_slots <= kExtendOneBlock * VEC) {
+    tq_prof_begin(TQK_PAGE_EXTEND, st);
+    const cudaError_t e = tq_launch_dependent(page_extend_kernel<true, true, VEC>, dim3(1), kExtendThreads, 0, st, a);
+    tq_prof_end(TQK_PAGE_EXTEND, st);
+    return e;
+  }
+  const int64_t want = n_slots / (4 * VEC * kExtendThreads) + 1, most = 4 * (int64_t)tq_device_sms(device);
+  tq_prof_begin(TQK_PAGE_SLOTS, st);
+  cudaError_t e = tq_launch_dependent(page_extend_kernel<true, false, VEC>, dim3((unsigned)(want < most ? want : most)), kExtendThreads, 0, st, a);
+  tq_prof_end(TQK_PAGE_SLOTS, st);
+  if (e != cudaSuccess) return e;
+  tq_prof_begin(TQK_PAGE_EXTEND, st);
+  e = tq_launch_dependent(page_extend_kernel<false, true, 1>, dim3(1), kExtendThreads, 0, st, a);
+  tq_prof_end(TQK_PAGE_EXTEND, st);
+  return e;
+}
+
 }  // namespace
 
 extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_lens, const int32_t *new_lens,
@@ -344,26 +391,10 @@ extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_le
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ExtendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, n_free, pages->n_blocks,
                n_slots / pages->n_kv_heads, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
-               seq_lens_out, granted, free_head_out, row_offsets, new_slots, FastDiv(pages->n_kv_heads),
-               FastDiv(pages->block_size)};
-  cudaError_t e;
-  if (n_slots <= kExtendOneBlock) {
-    tq_prof_begin(TQK_PAGE_EXTEND, s);
-    page_extend_kernel<true, true><<<1, kExtendThreads, 0, s>>>(a);
-    tq_prof_end(TQK_PAGE_EXTEND, s);
-    e = cudaGetLastError();
-  } else {
-    const int64_t want = n_slots / 4096 + 1, most = 4 * (int64_t)tq_sm_count();
-    tq_prof_begin(TQK_PAGE_SLOTS, s);
-    page_extend_kernel<true, false><<<(unsigned)(want < most ? want : most), kExtendThreads, 0, s>>>(a);
-    tq_prof_end(TQK_PAGE_SLOTS, s);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return tq_cuda_check(e, "page extend launch");
-    tq_prof_begin(TQK_PAGE_EXTEND, s);
-    page_extend_kernel<false, true><<<1, kExtendThreads, 0, s>>>(a);
-    tq_prof_end(TQK_PAGE_EXTEND, s);
-    e = cudaGetLastError();
-  }
+               seq_lens_out, granted, free_head_out, row_offsets, new_slots, FastDiv(), FastDiv(pages->block_size)};
+  const int vec = !tq_aligned(new_slots, 16) ? 1 : pages->n_kv_heads % 4 == 0 ? 4 : pages->n_kv_heads % 2 == 0 ? 2 : 1;
+  a.by_parts = FastDiv(pages->n_kv_heads / vec);
+  cudaError_t e = vec == 4 ? launch_extend<4>(a, n_slots, pages->device, s) : vec == 2 ? launch_extend<2>(a, n_slots, pages->device, s) : launch_extend<1>(a, n_slots, pages->device, s);
   return tq_cuda_check(e, "page extend launch");
 }
 
@@ -401,8 +432,8 @@ extern "C" tq_status tq_append_kv(const tq_pages *pages, const int32_t *seq_lens
                units, pages->block_table, seq_lens, granted, row_offsets, k_new, v_new, k_cache, v_cache, bounds};
   const unsigned grid = (unsigned)((units * pages->n_kv_heads + kAppendWarps - 1) / kAppendWarps);
   tq_prof_begin(TQK_APPEND_KV, s);
-  if (dtype == TQ_F32) append_kv_kernel<float><<<grid, 32 * kAppendWarps, 0, s>>>(a);
-  else append_kv_kernel<__nv_bfloat16><<<grid, 32 * kAppendWarps, 0, s>>>(a);
+  const cudaError_t e = tq_launch_dependent(dtype == TQ_F32 ? append_kv_kernel<float> : append_kv_kernel<__nv_bfloat16>, dim3(grid),
+                                            32 * kAppendWarps, 0, s, a);
   tq_prof_end(TQK_APPEND_KV, s);
-  return tq_cuda_check(cudaGetLastError(), "append launch");
+  return tq_cuda_check(e, "append launch");
 }

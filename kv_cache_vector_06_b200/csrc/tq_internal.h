@@ -86,6 +86,7 @@ class DeviceScope {
 tq_status tq_check_pages(const tq_pages *pages);
 tq_status tq_check_rows(tq_dtype dtype, int32_t d);            // row type and length
 tq_status tq_check_group(const tq_pages &pages, int32_t n_q_heads);  // query heads per KV head
+int tq_device_sms(int device);  // SMs of a device, asked for once (148 where the query fails)
 constexpr int kPagedMaxD = 256, kPagedMaxGroup = 16, kPagedMaxHeads = 65535;
 constexpr int64_t kPagedMaxTokens = 1 << 30;  // of a sequence: positions and what is added to them fit an int
 static inline bool tq_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -464,6 +464,12 @@ def search_topk(ctx: Context, q: torch.Tensor, db: Packed, k: int, n: int = None
     return out_scores, out_idx
 
 
+def _raw_stream(device: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 class Pages:
     """Paged-cache addressing (tq_pages): the block table [batch, max_blocks] and the cache's shape.
     Holds the table's tensor; the calls below run on its device."""
@@ -475,6 +481,7 @@ class Pages:
         self.batch, self.max_blocks = block_table.shape
         self.block_table = block_table
         self.n_kv_heads, self.block_size, self.n_blocks = n_kv_heads, block_size, n_blocks
+        self.rows = self.batch * n_kv_heads
         self._c = PagesC(self.device if block_table.is_cuda else -1, self.batch, n_kv_heads, block_size, self.max_blocks,
                          n_blocks, _dev(block_table, self.device, "block_table", torch.int32))
         self.ref = ctypes.byref(self._c)
@@ -484,18 +491,20 @@ class Pages:
         select_blocks chose."""
         return Pages(sel_table, 1, self.block_size, self.n_blocks * self.n_kv_heads)
 
-    def _lens(self, t, name: str, dtype=torch.int32, n: int = None):
-        if t.numel() != (self.batch if n is None else n):
-            raise ValueError(f"{name} must have {self.batch if n is None else n} entries")
-        return _dev(t, self.device, name, dtype)
+    def _arg(self, t: torch.Tensor, name: str, dtype, shape) -> int:
+        """Address of a contiguous tensor of this device with the given type and shape (an int: its number
+        of entries)."""
+        if (not isinstance(t, torch.Tensor) or t.get_device() != self.device or t.dtype is not dtype or not t.is_contiguous()
+                or (t.numel() if type(shape) is int else t.shape) != shape):
+            _dev(t, self.device, name, dtype)
+            raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+        return t.data_ptr()
 
-    def _rows(self, t, name: str, rows_per_block: int, d: int, dtype):
-        if t.shape[-1] != d or t.numel() != self.n_blocks * self.n_kv_heads * rows_per_block * d:
-            raise ValueError(f"{name} must be [{self.n_blocks}, {self.n_kv_heads}, {rows_per_block}, {d}]")
-        return _dev(t, self.device, name, dtype)
-
-    def _stream(self, stream):
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+    def _cache(self, t: torch.Tensor, name: str, per_block: int, d: int, dtype) -> int:
+        """Address of an array of `per_block` rows of d per (block, KV head)."""
+        if t.shape[-1] != d:
+            raise ValueError(f"{name} must be [{self.n_blocks}, {self.n_kv_heads}, {per_block}, {d}]")
+        return self._arg(t, name, dtype, self.n_blocks * self.n_kv_heads * per_block * d)
 
 
 def page_extend(pages: Pages, seq_lens, new_lens, free_blocks, free_head, n_rows: int = None, new_slots=None,
@@ -504,26 +513,26 @@ def page_extend(pages: Pages, seq_lens, new_lens, free_blocks, free_head, n_rows
     write them into pages.block_table, and return (new_slots int64 [n_rows * n_kv_heads], seq_lens_out,
     granted, free_head_out, row_offsets int64 [batch + 1]).  Outputs may be given; new_slots (or n_rows)
     bounds the rows of one call."""
-    dev = free_head.device
+    i32, i64, n = torch.int32, torch.int64, pages.batch
     if new_slots is None:
         if n_rows is None:
             raise ValueError("n_rows or new_slots is required")
-        new_slots = torch.empty(n_rows * pages.n_kv_heads, dtype=torch.int64, device=dev)
+        new_slots = torch.empty(n_rows * pages.n_kv_heads, dtype=i64, device=free_head.device)
     if seq_lens_out is None:
-        seq_lens_out = torch.empty(pages.batch, dtype=torch.int32, device=dev)
+        seq_lens_out = torch.empty(n, dtype=i32, device=free_head.device)
     if granted is None:
-        granted = torch.empty(pages.batch, dtype=torch.int32, device=dev)
+        granted = torch.empty(n, dtype=i32, device=free_head.device)
     if free_head_out is None:
-        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+        free_head_out = torch.empty(1, dtype=i32, device=free_head.device)
     if row_offsets is None:
-        row_offsets = torch.empty(pages.batch + 1, dtype=torch.int64, device=dev)
+        row_offsets = torch.empty(n + 1, dtype=i64, device=free_head.device)
+    n_free, n_slots, arg = free_blocks.numel(), new_slots.numel(), pages._arg
     _check(LIB.tq_page_extend(
-        pages.ref, pages._lens(seq_lens, "seq_lens"), pages._lens(new_lens, "new_lens"),
-        _dev(free_blocks, pages.device, "free_blocks", torch.int32), free_blocks.numel(),
-        pages._lens(free_head, "free_head", n=1), pages._lens(seq_lens_out, "seq_lens_out"),
-        pages._lens(granted, "granted"), pages._lens(free_head_out, "free_head_out", n=1),
-        pages._lens(row_offsets, "row_offsets", torch.int64, pages.batch + 1),
-        _dev(new_slots, pages.device, "new_slots", torch.int64), new_slots.numel(), pages._stream(stream)))
+        pages.ref, arg(seq_lens, "seq_lens", i32, n), arg(new_lens, "new_lens", i32, n),
+        arg(free_blocks, "free_blocks", i32, n_free), n_free, arg(free_head, "free_head", i32, 1),
+        arg(seq_lens_out, "seq_lens_out", i32, n), arg(granted, "granted", i32, n),
+        arg(free_head_out, "free_head_out", i32, 1), arg(row_offsets, "row_offsets", i64, n + 1),
+        arg(new_slots, "new_slots", i64, n_slots), n_slots, _raw_stream(pages.device, stream)))
     return new_slots, seq_lens_out, granted, free_head_out, row_offsets
 
 
@@ -532,44 +541,43 @@ def append_kv(pages: Pages, seq_lens, granted, row_offsets, k_new, v_new=None, k
     """tq_append_kv: write rows k_new, v_new ([n_rows, n_kv_heads, d], any row stride) into k_cache, v_cache
     ([n_blocks, n_kv_heads, block_size, d]) and keep bounds ([n_blocks, n_kv_heads, 2, d]); lengths, granted
     and row_offsets as page_extend returns them.  Without caches (None) only the bounds are kept."""
-    h = pages.n_kv_heads
-    rows = [k_new] if v_new is None else [k_new, v_new]
-    for t in rows:
-        if t.dim() != 3 or t.shape != k_new.shape or t.shape[1] != h or t.stride() != k_new.stride() or t.dtype != k_new.dtype:
-            raise ValueError(f"k_new and v_new must both be [n_rows, {h}, d] with one dtype and one row stride")
-    n, _, d = k_new.shape
-    if (d > 1 and k_new.stride(2) != 1) or (h > 1 and k_new.stride(1) != d):
+    n, h, d = k_new.shape if k_new.dim() == 3 else (0, -1, 0)
+    strides, dt, dev, b = k_new.stride(), k_new.dtype, pages.device, pages.batch
+    if h != pages.n_kv_heads or (v_new is not None and (v_new.shape != k_new.shape or v_new.stride() != strides
+                                                        or v_new.dtype is not dt)):
+        raise ValueError(f"k_new and v_new must both be [n_rows, {pages.n_kv_heads}, d] with one dtype and one row stride")
+    if (d > 1 and strides[2] != 1) or (h > 1 and strides[1] != d):
         raise ValueError("the heads of a row must lie side by side")
-    dt, dev = k_new.dtype, pages.device
-    ld = k_new.stride(0) if n > 1 else h * d
-    ptr = lambda t, name, per: None if t is None else pages._rows(t, name, per, d, dt)  # noqa: E731
+    if k_new.get_device() != dev or (v_new is not None and v_new.get_device() != dev):
+        raise ValueError(f"k_new and v_new must be CUDA tensors on device {dev}")
+    arg, cache, i32 = pages._arg, pages._cache, torch.int32
     _check(LIB.tq_append_kv(
-        pages.ref, pages._lens(seq_lens, "seq_lens"), pages._lens(granted, "granted"),
-        pages._lens(row_offsets, "row_offsets", torch.int64, pages.batch + 1),
-        _dev(k_new, dev, "k_new", contiguous=False), None if v_new is None else _dev(v_new, dev, "v_new", contiguous=False),
-        _dtype_code(k_new), d, n, ld, ptr(k_cache, "k_cache", pages.block_size), ptr(v_cache, "v_cache", pages.block_size),
-        ptr(bounds, "bounds", 2), pages._stream(stream)))
+        pages.ref, arg(seq_lens, "seq_lens", i32, b), arg(granted, "granted", i32, b),
+        arg(row_offsets, "row_offsets", torch.int64, b + 1), k_new.data_ptr(), None if v_new is None else v_new.data_ptr(),
+        _dtype_code(k_new), d, n, strides[0] if n > 1 else h * d,
+        None if k_cache is None else cache(k_cache, "k_cache", pages.block_size, d, dt),
+        None if v_cache is None else cache(v_cache, "v_cache", pages.block_size, d, dt),
+        None if bounds is None else cache(bounds, "bounds", 2, d, dt), _raw_stream(dev, stream)))
 
 
-def _queries(pages: Pages, q):
-    if q.dim() != 3 or q.shape[0] != pages.batch:
+def _queries(pages: Pages, q: torch.Tensor):
+    """(address, query heads, d) of q [batch, n_q_heads, d]."""
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != pages.batch:
         raise ValueError(f"q must be [{pages.batch}, n_q_heads, d]")
-    return _dev(q, pages.device, "q")
+    return pages._arg(q, "q", q.dtype, shape), shape[1], shape[2]
 
 
 def block_scores(pages: Pages, seq_lens, q, bounds, out=None, stream=None):
     """tq_block_scores: upper bounds fp32 [batch * n_kv_heads, max_blocks] of the products of q
     ([batch, n_q_heads, d]) with the keys of every block, from the bounds that append_kv keeps."""
-    rows = pages.batch * pages.n_kv_heads
-    qp = _queries(pages, q)
+    qp, hq, d = _queries(pages, q)
     if out is None:
-        out = torch.empty(rows, pages.max_blocks, dtype=torch.float32, device=q.device)
-    if tuple(out.shape) != (rows, pages.max_blocks):
-        raise ValueError(f"out must be [{rows}, {pages.max_blocks}]")
+        out = torch.empty(pages.rows, pages.max_blocks, dtype=torch.float32, device=q.device)
     _check(LIB.tq_block_scores(
-        pages.ref, pages._lens(seq_lens, "seq_lens"), qp, _dtype_code(q), q.shape[1], q.shape[2],
-        pages._rows(bounds, "bounds", 2, q.shape[2], q.dtype), _dev(out, pages.device, "out", torch.float32),
-        pages._stream(stream)))
+        pages.ref, pages._arg(seq_lens, "seq_lens", torch.int32, pages.batch), qp, _dtype_code(q), hq, d,
+        pages._cache(bounds, "bounds", 2, d, q.dtype),
+        pages._arg(out, "out", torch.float32, (pages.rows, pages.max_blocks)), _raw_stream(pages.device, stream)))
     return out
 
 
@@ -579,18 +587,16 @@ def select_blocks(pages: Pages, seq_lens, scores, n_keep: int, n_first: int = 1,
     (sequence, KV head), n_keep in all, as a block table [batch * n_kv_heads, n_keep] and the tokens in it.
     pages.selected(table) reads the same cache through it; for make_attn_desc it is the block_table of
     batch * n_kv_heads sequences with n_kv_heads = 1."""
-    rows = pages.batch * pages.n_kv_heads
-    if tuple(scores.shape) != (rows, pages.max_blocks):
-        raise ValueError(f"scores must be [{rows}, {pages.max_blocks}]")
     if table is None:
-        table = torch.empty(rows, max(n_keep, 0), dtype=torch.int32, device=scores.device)
+        table = torch.empty(pages.rows, max(n_keep, 0), dtype=torch.int32, device=scores.device)
     if lens is None:
-        lens = torch.empty(rows, dtype=torch.int32, device=scores.device)
-    if tuple(table.shape) != (rows, max(n_keep, 0)):
-        raise ValueError(f"table must be [{rows}, {n_keep}]")
+        lens = torch.empty(pages.rows, dtype=torch.int32, device=scores.device)
+    arg, i32 = pages._arg, torch.int32
     _check(LIB.tq_select_blocks(
-        pages.ref, pages._lens(seq_lens, "seq_lens"), _dev(scores, pages.device, "scores", torch.float32), n_keep, n_first,
-        n_last, _dev(table, pages.device, "table", torch.int32), pages._lens(lens, "lens", n=rows), pages._stream(stream)))
+        pages.ref, arg(seq_lens, "seq_lens", i32, pages.batch),
+        arg(scores, "scores", torch.float32, (pages.rows, pages.max_blocks)), n_keep, n_first, n_last,
+        arg(table, "table", i32, (pages.rows, max(n_keep, 0))), arg(lens, "lens", i32, pages.rows),
+        _raw_stream(pages.device, stream)))
     return table, lens
 
 
@@ -605,18 +611,17 @@ def attend_paged(pages: Pages, seq_lens, max_seq_len: int, q, k_cache, v_cache, 
     """tq_attend_paged: attention of one new token per sequence, q [batch, n_q_heads, d], over the
     uncompressed caches [n_blocks, n_kv_heads, block_size, d] of q's dtype.  out: fp32 (the default) or
     q's dtype."""
-    qp = _queries(pages, q)
-    _, hq, d = q.shape
+    qp, hq, d = _queries(pages, q)
+    dev, dt = pages.device, q.dtype
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    w, wb = _workspace(attend_paged_workspace_size(pages, max_seq_len, hq, d), pages.device, ws)
+    if ws is None:
+        ws = torch.empty(attend_paged_workspace_size(pages, max_seq_len, hq, d), dtype=torch.uint8, device=q.device)
     _check(LIB.tq_attend_paged(
-        pages.ref, pages._lens(seq_lens, "seq_lens"), max_seq_len, qp,
-        pages._rows(k_cache, "k_cache", pages.block_size, d, q.dtype),
-        pages._rows(v_cache, "v_cache", pages.block_size, d, q.dtype), _dtype_code(q), hq, d, scale,
-        _dev(out, pages.device, "out"), _dtype_code(out), w, wb, pages._stream(stream)))
+        pages.ref, pages._arg(seq_lens, "seq_lens", torch.int32, pages.batch), max_seq_len, qp,
+        pages._cache(k_cache, "k_cache", pages.block_size, d, dt), pages._cache(v_cache, "v_cache", pages.block_size, d, dt),
+        _dtype_code(q), hq, d, scale, pages._arg(out, "out", out.dtype, q.shape), _dtype_code(out),
+        _dev(ws, dev, "ws"), ws.numel() * ws.element_size(), _raw_stream(dev, stream)))
     return out
 
 
