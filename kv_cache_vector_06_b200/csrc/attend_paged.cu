@@ -74,9 +74,11 @@ struct Stream {
                                        int lane) {
     constexpr int kT = S::kTok / 8;
     const int c = lane & 3, r = lane >> 2;
-    float s[kT][4];
+    // chunk 4 kg + c of token r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
+    const unsigned at[2] = {r * S::kRow + 16 * key_chunk(r, c), r * S::kRow + 16 * key_chunk(r, 4 + c)};
+    float s[kBf ? kT : 2][4];  // fp32: two sums, of every other group, so that the products wait less for one another
 #pragma unroll
-    for (int t = 0; t < kT; ++t)
+    for (int t = 0; t < (kBf ? kT : 2); ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
@@ -90,7 +92,7 @@ struct Stream {
 #pragma unroll
       for (int t = 0; t < kT; ++t) {
         uint32_t k[4];
-        lds128(k, kbase + (8 * t + r) * S::kRow + 16 * key_chunk(r, 4 * kg + c));
+        lds128(k, kbase + at[kg & 1] + 8 * t * S::kRow + 128 * (kg >> 1));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           if constexpr (kBf) {
@@ -98,19 +100,23 @@ struct Stream {
             else mma_bf16(s[t], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, k[2 * u], k[2 * u + 1]);
           } else {
             uint32_t h0, l0, h1, l1;
-            split_tf32(k[2 * u], h0, l0);
-            split_tf32(k[2 * u + 1], h1, l1);
+            split_tf32_cut(k[2 * u], h0, l0);
+            split_tf32_cut(k[2 * u + 1], h1, l1);
             if constexpr (WIDE) {
-              mma_tf32(s[t], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
-              mma_tf32(s[t], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
-              mma_tf32(s[t], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
+              mma_tf32(s[kg & 1], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
+              mma_tf32(s[kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
+              mma_tf32(s[kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
             } else {
-              mma_tf32(s[t], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
-              mma_tf32(s[t], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
+              mma_tf32(s[kg & 1], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
+              mma_tf32(s[kg & 1], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
             }
           }
         }
       }
+    }
+    if constexpr (!kBf) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
     }
     // logits in units of log2, masked; lane: head r (+ 8), tokens 8 t + 2 c, 8 t + 2 c + 1
     float p[kH][kT][2];
@@ -208,8 +214,8 @@ struct Stream {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t h0, l0, h1, l1;
-          split_tf32(v0[i], h0, l0);
-          split_tf32(v1[i], h1, l1);
+          split_tf32_cut(v0[i], h0, l0);
+          split_tf32_cut(v1[i], h1, l1);
           float(&acc)[4] = o[4 * g + i];
           if constexpr (WIDE) {
             mma_tf32(acc, pl[0][0], pl[kH - 1][0], pl[0][1], pl[kH - 1][1], h0, h1);
@@ -333,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
 #pragma unroll
       for (int x = 0; x < S::kTok * S::kCh / 32; ++x) {
         const int idx = lane + 32 * x, r = idx / S::kCh, ch = idx % S::kCh;
-        const int64_t base = whole ? off + (int64_t)r * esz_row : __shfl_sync(TQ_FULL_MASK, off, r);
-        const bool in = ((valid >> r) & 1u) && ch < dch;
-        const int64_t src = in ? base + 16 * ch : 0;
-        cp16(kb + r * S::kRow + 16 * key_chunk(r, ch), static_cast<const char *>(a.k) + src, in ? 16 : 0);
-        cp16(vb + r * S::kRow + 16 * value_chunk<T>(r, ch), static_cast<const char *>(a.v) + src, in ? 16 : 0);
+        const int64_t base = whole ? off + r * esz_row : __shfl_sync(TQ_FULL_MASK, off, r);
+        const int64_t src = base + 16 * min(ch, dch - 1);  // inside the cache; read where the token is there
+        const int bytes = ((valid >> r) & 1u) && ch < dch ? 16 : 0;
+        cp16(kb + r * S::kRow + 16 * key_chunk(r, ch), static_cast<const char *>(a.k) + src, bytes);
+        cp16(vb + r * S::kRow + 16 * value_chunk<T>(r, ch), static_cast<const char *>(a.v) + src, bytes);
       }
     };
     int e[S::kStages];

@@ -16,20 +16,174 @@ struct BlockScoreArgs {
 // Steps that a row costs a warp beside its own: its queries and its first loads.
 constexpr int kRowCost = 2;
 
-// max_c over a box: max(q_c lower_c, q_c upper_c) = min(q_c, 0) lower_c + max(q_c, 0) upper_c, so the
-// scores of a step's blocks are two products over d, one with each half of the query.  Bound: 2 d values
-// per block, read once for the whole group: HBM.  The loads, the operands' layout and the division of the
-// work are those of the paged attention, a step being kTok blocks; every warp works alone.
+// max_c over a box: max(q_c lower_c, q_c upper_c) = min(q_c, 0) lower_c + max(q_c, 0) upper_c.
+//
+// bf16: a step's scores are two products over d, one with each half of the query, on the tensor cores.
+// Lane: chunk 4 kg + lane % 4 of heads lane / 4 (+ 8).
+template <typename T, int D, bool WIDE>
+struct Scorer {
+  using S = Shape<T, D>;
+  static constexpr int kH = WIDE ? 2 : 1, kKg = S::kCh / 4, kT = S::kTok / 8;
+  static constexpr bool kQInRegs = kKg * kH <= 16;
+  uint32_t q[kQInRegs ? kKg : 1][2][kH][4];
+
+  static __device__ __forceinline__ int chunk(int row, int ch) { return key_chunk(row, ch); }
+  __device__ __forceinline__ void halves(uint32_t (&f)[2][kH][4], const uint4 (&v)[kH]) {
+#pragma unroll
+    for (int x = 0; x < kH; ++x) {
+      const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const __nv_bfloat162 p = reinterpret_cast<const __nv_bfloat162 &>(w[y]), z = __floats2bfloat162_rn(0.f, 0.f);
+        const __nv_bfloat162 lo = __hmin2(p, z), hi = __hmax2(p, z);
+        f[0][x][y] = reinterpret_cast<const uint32_t &>(lo);
+        f[1][x][y] = reinterpret_cast<const uint32_t &>(hi);
+      }
+    }
+  }
+  uint4 raw[kQInRegs ? kKg : 1][kH];
+  __device__ __forceinline__ void ask(const BlockScoreArgs &a, int64_t row, int lane) {
+    if constexpr (kQInRegs) {
+#pragma unroll
+      for (int kg = 0; kg < kKg; ++kg) load_q<T, kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
+    }
+  }
+  __device__ __forceinline__ void prepare() {
+    if constexpr (kQInRegs) {
+#pragma unroll
+      for (int kg = 0; kg < kKg; ++kg) halves(q[kg], raw[kg]);
+    }
+  }
+  // The score of block `k` of the step, in the lanes that have one (k >= 0).
+  __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t row, unsigned lower, unsigned upper, int lane, int &k) {
+    const int c = lane & 3, r = lane >> 2;
+    // chunk 4 kg + c of block r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
+    const unsigned at[2] = {r * S::kRow + 16 * key_chunk(r, c), r * S::kRow + 16 * key_chunk(r, 4 + c)};
+    float s[2][kT][4];
+#pragma unroll
+    for (int x = 0; x < 8 * kT; ++x) s[x / (4 * kT)][x / 4 % kT][x % 4] = 0.f;
+#pragma unroll
+    for (int kg = 0; kg < kKg; ++kg) {
+      if constexpr (!kQInRegs) {
+        load_q<T, kH>(raw[0], a.q, row, a.group, a.d, kg, lane);
+        halves(q[0], raw[0]);
+      }
+#pragma unroll
+      for (int up = 0; up < 2; ++up) {
+        const auto &g = q[kQInRegs ? kg : 0][up];
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          uint32_t x[4];
+          lds128(x, (up ? upper : lower) + at[kg & 1] + 8 * t * S::kRow + 128 * (kg >> 1));
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            mma_bf16(s[up][t], g[0][2 * u], WIDE ? g[kH - 1][2 * u] : 0u, g[0][2 * u + 1], WIDE ? g[kH - 1][2 * u + 1] : 0u,
+                     x[2 * u], x[2 * u + 1]);
+        }
+      }
+    }
+    // the largest over the heads: lane holds heads r (and 8 + r) of blocks 8 t + 2 c, 8 t + 2 c + 1
+    float mine = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float v = r < a.group ? s[0][t][x] + s[1][t][x] : -INFINITY;
+        if (WIDE && r + 8 < a.group) v = fmaxf(v, s[0][t][2 + x] + s[1][t][2 + x]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(TQ_FULL_MASK, v, o));
+        if (r == 2 * t + x) mine = v;
+      }
+    k = r < 2 * kT ? 8 * (r >> 1) + 2 * c + (r & 1) : -1;
+    return mine;
+  }
+};
+
+// fp32: on the CUDA cores, where a term is a select and a multiply-add.  (TF32 parts on the tensor cores took
+// 1.4 times the instructions for 4 heads, and a tensor core cuts each sum that it returns: these sums
+// grow from term to term, and were 1.2e-6 off instead of 4e-8.)  A row of D / 4 lanes holds four channels
+// (D = 256: twice four) of every head; four heads at a time, the lanes' sums over a step's 8 blocks are
+// exchanged until each lane has one whole sum.
+template <int D, bool WIDE>
+struct Scorer<float, D, WIDE> {
+  using S = Shape<float, D>;
+  static constexpr int kLanes = D == 64 ? 16 : 32;  // lanes of a row
+  static constexpr int kAt = 32 / kLanes;           // blocks at once
+  static constexpr int kEach = 8 / kAt;             // blocks of a lane
+  static constexpr int kVec = D == 256 ? 2 : 1;
+  static constexpr int kHeads = WIDE ? 16 : 8;
+  float4 q[kHeads][kVec];
+
+  static __device__ __forceinline__ int chunk(int, int ch) { return ch; }
+  __device__ __forceinline__ void ask(const BlockScoreArgs &a, int64_t row, int lane) {
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        const int ch = lane % kLanes + 32 * v;
+        q[h][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h < a.group && 4 * ch < a.d)
+          q[h][v] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + (row * a.group + h) * a.d) + ch);
+      }
+  }
+  __device__ __forceinline__ void prepare() {}
+  static __device__ __forceinline__ float pick(float x, float lo, float hi, float s) { return fmaf(x, x >= 0.f ? hi : lo, s); }
+  __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t, unsigned lower, unsigned upper, int lane, int &k) {
+    const int v = lane % kLanes;
+    float best = -INFINITY;
+#pragma unroll
+    for (int h0 = 0; h0 < kHeads; h0 += 4) {
+      if (h0 >= a.group) break;
+      float s[4 * kEach];  // [head][block]
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kVec; ++w) {
+          uint32_t l[4], u[4];
+          lds128(l, lower + i * kAt * S::kRow + 16 * (lane + 32 * w));
+          lds128(u, upper + i * kAt * S::kRow + 16 * (lane + 32 * w));
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float4 x = q[h0 + h][w];
+            t[h] = pick(x.x, __uint_as_float(l[0]), __uint_as_float(u[0]), t[h]);
+            t[h] = pick(x.y, __uint_as_float(l[1]), __uint_as_float(u[1]), t[h]);
+            t[h] = pick(x.z, __uint_as_float(l[2]), __uint_as_float(u[2]), t[h]);
+            t[h] = pick(x.w, __uint_as_float(l[3]), __uint_as_float(u[3]), t[h]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) s[h * kEach + i] = t[h];
+      }
+      // lane v of a row ends with the sum over the row's lanes of s[v]
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const bool high = lane & o;
+          const float give = high ? s[i] : s[i + o], keep = high ? s[i + o] : s[i];
+          s[i] = keep + __shfl_xor_sync(TQ_FULL_MASK, give, o);
+        }
+      float x = h0 + v / kEach < a.group ? s[0] : -INFINITY;
+#pragma unroll
+      for (int o = kEach; o < kLanes; o <<= 1) x = fmaxf(x, __shfl_xor_sync(TQ_FULL_MASK, x, o));
+      best = fmaxf(best, x);
+    }
+    k = v < kEach ? lane / kLanes + kAt * v : -1;
+    return best;
+  }
+};
+
+// Bound: 2 d values per block, read once for the whole group: HBM.  The loads and the division of the work
+// are those of the paged attention, a step being kTok blocks; every warp works alone.
 template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kernel(BlockScoreArgs a) {
   using S = Shape<T, D>;
-  constexpr bool kBf = sizeof(T) == 2;
-  constexpr int kH = WIDE ? 2 : 1, kParts = kBf ? 1 : 2, kKg = S::kCh / 4, kT = S::kTok / 8;
-  constexpr bool kQInRegs = kKg * kH * kParts * 4 <= 64;
+  using Sc = Scorer<T, D, WIDE>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Place place[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, r = lane >> 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
@@ -52,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
   int64_t unit = place[warp].unit - (int64_t)h * (steps + kRowCost);  // place in the row, its cost in front
   const unsigned ring = smem_addr(smem) + warp * S::kRing;
   const int row_bytes = a.d * (int)sizeof(T), dch = row_bytes / 16;
+  Sc scorer;
 
   for (int64_t pos = begin; pos < end;) {
     const int64_t span = min(steps + kRowCost - unit, end - pos);
@@ -72,32 +227,23 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
 #pragma unroll
       for (int x = 0; x < S::kTok * S::kCh / 32; ++x) {
         const int idx = lane + 32 * x, k = idx / S::kCh, ch = idx % S::kCh;
-        const int64_t base = __shfl_sync(TQ_FULL_MASK, off, k);
-        const bool in = ((valid >> k) & 1u) && ch < dch;
-        const char *src = static_cast<const char *>(a.bounds) + (in ? base + 16 * ch : 0);
-        cp16(lb + k * S::kRow + 16 * key_chunk(k, ch), src, in ? 16 : 0);
-        cp16(ub + k * S::kRow + 16 * key_chunk(k, ch), src + (in ? row_bytes : 0), in ? 16 : 0);
+        const int bytes = ((valid >> k) & 1u) && ch < dch ? 16 : 0;
+        const char *src = static_cast<const char *>(a.bounds) + (__shfl_sync(TQ_FULL_MASK, off, k) + 16 * min(ch, dch - 1));
+        cp16(lb + k * S::kRow + 16 * Sc::chunk(k, ch), src, bytes);
+        cp16(ub + k * S::kRow + 16 * Sc::chunk(k, ch), src + row_bytes, bytes);
       }
     };
     int e[S::kStages];
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
-    uint4 raw[kQInRegs ? kKg : 1][kH];  // asked for before the bounds, so that it does not queue behind them
-    if constexpr (kQInRegs) {
-#pragma unroll
-      for (int kg = 0; kg < kKg; ++kg) load_q<T, kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
-    }
+    scorer.ask(a, row, lane);  // before the bounds, so that it does not queue behind them
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) {
       if (i < n) issue(i, e[i]);
       cp_commit();
     }
     int next = e[S::kStages - 1];
-    uint32_t qf[kQInRegs ? kKg : 1][kH][kParts][4];
-    if constexpr (kQInRegs) {
-#pragma unroll
-      for (int kg = 0; kg < kKg; ++kg) make_q<T, kH>(qf[kg], raw[kg]);
-    }
+    scorer.prepare();
     for (int i = 0; i < n; ++i) {
       cp_wait<S::kStages - 2>();
       __syncwarp();  // this step's copies of every lane have landed; the last step's stage is free
@@ -106,78 +252,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
       next = entry(i + S::kStages);
       const int stage = i % S::kStages;
       const unsigned lb = ring + stage * S::kStage;
-      const uint32_t valid = masks[warp][stage];
-      float s[kT][4];
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[t][x] = 0.f;
-#pragma unroll
-      for (int kg = 0; kg < kKg; ++kg) {
-        if constexpr (!kQInRegs) {
-          load_q<T, kH>(raw[0], a.q, row, a.group, a.d, kg, lane);
-          make_q<T, kH>(qf[0], raw[0]);
-        }
-        const auto &f = qf[kQInRegs ? kg : 0];
-#pragma unroll
-        for (int up = 0; up < 2; ++up) {
-          // min(q, 0) for the lower bounds, max(q, 0) for the upper ones
-          uint32_t g[kH][kParts][4];
-#pragma unroll
-          for (int x = 0; x < kH; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if constexpr (kBf) {
-                const __nv_bfloat162 w = reinterpret_cast<const __nv_bfloat162 &>(f[x][0][y]), z = __floats2bfloat162_rn(0.f, 0.f);
-                const __nv_bfloat162 v = up ? __hmax2(w, z) : __hmin2(w, z);
-                g[x][0][y] = reinterpret_cast<const uint32_t &>(v);
-              } else {
-                const uint32_t neg = (uint32_t)((int32_t)f[x][0][y] >> 31), on = up ? ~neg : neg;
-                g[x][0][y] = f[x][0][y] & on;
-                g[x][kParts - 1][y] = f[x][kParts - 1][y] & on;
-              }
-            }
-#pragma unroll
-          for (int t = 0; t < kT; ++t) {
-            uint32_t k[4];
-            lds128(k, lb + up * S::kTok * S::kRow + (8 * t + r) * S::kRow + 16 * key_chunk(r, 4 * kg + c));
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if constexpr (kBf) {
-                mma_bf16(s[t], g[0][0][2 * u], WIDE ? g[kH - 1][0][2 * u] : 0u, g[0][0][2 * u + 1],
-                         WIDE ? g[kH - 1][0][2 * u + 1] : 0u, k[2 * u], k[2 * u + 1]);
-              } else {
-                uint32_t h0, l0, h1, l1;
-                split_tf32(k[2 * u], h0, l0);
-                split_tf32(k[2 * u + 1], h1, l1);
-                if constexpr (WIDE) {
-                  mma_tf32(s[t], g[0][kParts - 1][2 * u], g[kH - 1][kParts - 1][2 * u], g[0][kParts - 1][2 * u + 1],
-                           g[kH - 1][kParts - 1][2 * u + 1], h0, h1);
-                  mma_tf32(s[t], g[0][0][2 * u], g[kH - 1][0][2 * u], g[0][0][2 * u + 1], g[kH - 1][0][2 * u + 1], l0, l1);
-                  mma_tf32(s[t], g[0][0][2 * u], g[kH - 1][0][2 * u], g[0][0][2 * u + 1], g[kH - 1][0][2 * u + 1], h0, h1);
-                } else {
-                  mma_tf32(s[t], g[0][0][2 * u], 0u, g[0][0][2 * u + 1], 0u, l0, l1);
-                  mma_tf32(s[t], g[0][0][2 * u], g[0][kParts - 1][2 * u], g[0][0][2 * u + 1], g[0][kParts - 1][2 * u + 1], h0, h1);
-                }
-              }
-            }
-          }
-        }
-      }
-      // the largest over the heads: lane holds heads r (and 8 + r) of blocks 8 t + 2 c, 8 t + 2 c + 1
-      float mine = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float v = r < a.group ? (WIDE || kBf ? s[t][x] : s[t][x] + s[t][2 + x]) : -INFINITY;
-          if (WIDE && r + 8 < a.group) v = fmaxf(v, s[t][2 + x]);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(TQ_FULL_MASK, v, o));
-          if (r == 2 * t + x) mine = v;
-        }
-      const int k = 8 * (r >> 1) + 2 * c + (r & 1), j = (first + i) * S::kTok + k;
-      if (r < 2 * kT && j < a.max_blocks) a.out[row * a.max_blocks + j] = (valid >> k) & 1u ? mine : -INFINITY;
+      int k;
+      const float s = scorer.step(a, row, lb, lb + S::kTok * S::kRow, lane, k);
+      const int j = (first + i) * S::kTok + k;
+      if (k >= 0 && j < a.max_blocks) a.out[row * a.max_blocks + j] = (masks[warp][stage] >> k) & 1u ? s : -INFINITY;
     }
     cp_wait<0>();
     __syncwarp();
@@ -220,9 +298,10 @@ struct SelectArgs {
 };
 
 constexpr int kSelectThreads = 512;
+constexpr int kSelectList = 2048;  // keys of one leading digit that are put aside
 
 // A float's order as an unsigned integer: larger floats have larger keys, -0 and +0 the same one, and
-// NaN the key of -infinity.
+// NaN the key of -infinity.  Never 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
   const uint32_t u = __float_as_uint(f != f ? -INFINITY : f + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -256,18 +335,64 @@ __device__ __forceinline__ void block_scan(int a, int b, int &ea, int &eb, int &
   tb = (int)(t >> 16);
 }
 
-// One block per (sequence, KV head).  Radix selection: the key of the last block chosen is found
-// eight bits at a time from counts of the keys that share the bits found so far; then one pass in
-// index order writes the blocks above that key and the first ones at it.  Each thread holds PER
+// The 2048 counts of `hist`, largest digit first, cut where `need` of them are passed: the digit, and how many
+// of its keys are still needed.  Leaves the counts at zero.
+__device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &rest) {
+  __shared__ int wsum[kSelectThreads / 32];
+  __shared__ int found, left;
+  constexpr int kPer = 2048 / kSelectThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = 2047 - kPer * threadIdx.x;
+  int4 *mine = reinterpret_cast<int4 *>(hist + top - 3);
+  static_assert(kPer == 4, "one int4 of counts per thread");
+  const int4 v = *mine;
+  *mine = make_int4(0, 0, 0, 0);
+  const int cnt[4] = {v.w, v.z, v.y, v.x};
+  const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+  int s = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(TQ_FULL_MASK, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) wsum[warp] = s;
+  __syncthreads();
+  int before = s - sum;
+#pragma unroll
+  for (int i = 0; i < kSelectThreads / 32; ++i)
+    if (i < warp) before += wsum[i];
+  int r = need - before;
+  if (r > 0 && r <= sum) {
+    int i = 0;
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (i == x && r > cnt[x]) {
+        r -= cnt[x];
+        ++i;
+      }
+    found = top - i;
+    left = r;
+  }
+  __syncthreads();
+  digit = found;
+  rest = left;
+}
+
+// One block per (sequence, KV head).  Radix selection: the key of the last block chosen is found from
+// counts of its digits (11, 11 and 10 bits), the leading one over all keys; the keys that share it are then
+// put aside, a few hundred of them where scores spread, and the other digits are found among those.  One
+// pass in index order writes the blocks above that key and the first ones at it.  Each thread holds PER
 // consecutive keys, so that index order is thread order; rows longer than a block's PER * 512 keys go
-// through in chunks, read again for each pass.
+// through in chunks, read again for each pass, and so do those where a digit's keys outgrow the list.
 template <int PER>
 __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArgs a) {
   constexpr int kChunk = PER * kSelectThreads;
-  __shared__ int hist[256];
-  __shared__ uint32_t found;
-  __shared__ int left;
+  __shared__ __align__(16) int hist[2048];
+  __shared__ uint32_t list[kSelectList];
+  __shared__ int listed;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 2048 / kSelectThreads; ++i) hist[threadIdx.x + i * kSelectThreads] = 0;
+  if (threadIdx.x == 0) listed = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
   const int b = (int)(blockIdx.x / (unsigned)a.heads), h = (int)(blockIdx.x - (unsigned)b * (unsigned)a.heads);
@@ -302,9 +427,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
         k[i + 2] = order_key(v.z);
         k[i + 3] = order_key(v.w);
       }
+      if (j < lo || j + PER > hi) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (j + i < lo || j + i >= hi) k[i] = 0;
+        for (int i = 0; i < PER; ++i)
+          if (j + i < lo || j + i >= hi) k[i] = 0;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < PER; ++i) k[i] = j + i >= lo && j + i < hi ? order_key(__ldg(scores + j + i)) : 0;
@@ -312,72 +439,81 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
   };
   const bool once = n <= kChunk;
   if (once) load(0);
+  __syncthreads();  // the counts are zero
   uint32_t key = 0xffffffffu;  // above every key, where only the forced blocks are kept
   int equal = 0;               // blocks at exactly `key` to take, the first ones
-  int need = a.keep - a.first - a.last;
+  const int need = a.keep - a.first - a.last;
   if (need > 0) {
-    key = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j0 = 0; j0 < n; j0 += kChunk) {
-        if (!once) load(j0);
+    int digit;
+    for (int j0 = 0; j0 < n; j0 += kChunk) {
+      if (!once) load(j0);
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (k[i] != 0 && (shift == 24 || ((k[i] ^ key) >> ((shift + 8) & 31)) == 0)) atomicAdd(&hist[(k[i] >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (threadIdx.x < 32) {  // lane l: digits 255 - 8 l down to 248 - 8 l
-        int cnt[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += cnt[i] = hist[255 - 8 * threadIdx.x - i];
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(TQ_FULL_MASK, incl, o);
-          if ((int)threadIdx.x >= o) incl += u;
-        }
-        int rest = need - (incl - sum);
-        if (rest > 0 && rest <= sum) {
-          int i = 0;
-#pragma unroll
-          for (int x = 0; x < 7; ++x)
-            if (i == x && rest > cnt[x]) {
-              rest -= cnt[x];
-              ++i;
-            }
-          found = key | ((uint32_t)(255 - 8 * threadIdx.x - i) << shift);
-          left = rest;
-        }
-      }
-      __syncthreads();
-      key = found;
-      need = left;
+      for (int i = 0; i < PER; ++i)
+        if (k[i] != 0) atomicAdd(&hist[k[i] >> 21], 1);
     }
-    equal = need;
+    __syncthreads();
+    cut_digit(hist, need, digit, equal);
+    key = (uint32_t)digit << 21;
+    for (int j0 = 0; j0 < n; j0 += kChunk) {
+      if (!once) load(j0);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (k[i] != 0 && (k[i] ^ key) < (1u << 21)) {
+          const int at = atomicAdd(&listed, 1);
+          if (at < kSelectList) list[at] = k[i];
+        }
+    }
+    __syncthreads();
+    const int count = listed;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      const int shift = pass ? 0 : 10, above = pass ? 10 : 21;
+      const uint32_t mask = pass ? 1023u : 2047u;
+      if (count <= kSelectList) {
+        for (int i = threadIdx.x; i < count; i += kSelectThreads)
+          if (((list[i] ^ key) >> above) == 0) atomicAdd(&hist[(list[i] >> shift) & mask], 1);
+      } else {
+        for (int j0 = 0; j0 < n; j0 += kChunk) {
+          if (!once) load(j0);
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (k[i] != 0 && ((k[i] ^ key) >> above) == 0) atomicAdd(&hist[(k[i] >> shift) & mask], 1);
+        }
+      }
+      __syncthreads();
+      cut_digit(hist, equal, digit, equal);
+      key |= (uint32_t)digit << shift;
+    }
   }
   int at = 0, seen = 0;  // blocks written, blocks at `key` passed, before this chunk
   for (int j0 = 0; j0 < n; j0 += kChunk) {
     if (!once) load(j0);
     const int j = j0 + PER * threadIdx.x;
-    int above = 0, ties = 0;
+    uint32_t above = 0, ties = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const bool forced = j + i < n && (j + i < lo || j + i >= hi);
-      above += forced || k[i] > key;
-      ties += k[i] == key;
+      above |= (k[i] > key ? 1u : 0u) << i;
+      ties |= (k[i] == key ? 1u : 0u) << i;
+    }
+    if (j < lo || j + PER > hi) {  // the forced ones
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (j + i < n && (j + i < lo || j + i >= hi)) above |= 1u << i;
     }
     int ea, eb, ta, tb;
-    block_scan(above, ties, ea, eb, ta, tb);
-    // ties before this thread that were taken: the first `equal` of the row
-    int t = seen + eb;
-    int p = at + ea + min(t, equal) - min(seen, equal);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool forced = j + i < n && (j + i < lo || j + i >= hi);
-      const bool tie = k[i] == key;
-      if (forced || k[i] > key || (tie && t < equal)) store(p++, j + i);
-      t += tie;
+    block_scan(__popc(above), __popc(ties), ea, eb, ta, tb);
+    // of the row's ties the first `equal` are taken: so many of this thread's
+    const int first = seen + eb;
+    int p = at + ea + min(first, equal) - min(seen, equal);
+    int room = max(equal - first, 0);
+    while (ties) {
+      const uint32_t bit = ties & (0u - ties);
+      if (room-- > 0) above |= bit;
+      ties ^= bit;
+    }
+    while (above) {
+      store(p++, j + __ffs(above) - 1);
+      above &= above - 1;
     }
     at += ta + min(seen + tb, equal) - min(seen, equal);
     seen += tb;

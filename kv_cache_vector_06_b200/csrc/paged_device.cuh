@@ -67,6 +67,13 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &l
   hi = tf32(__uint_as_float(x));
   lo = tf32(__uint_as_float(x) - __uint_as_float(hi));
 }
+// The same for the cache's own values, of which there are many, in two instructions: the products read the
+// first 11 bits of an operand, so x is its own head and the tail needs no rounding; cut to 11 bits, it
+// leaves 2^-20 of x at most.
+__device__ __forceinline__ void split_tf32_cut(uint32_t x, uint32_t &hi, uint32_t &lo) {
+  hi = x;
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(x & 0xffffe000u));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return reinterpret_cast<const uint32_t &>(v);

@@ -51,7 +51,7 @@ tq_status tq_check_group(const tq_pages &p, int32_t n_q_heads) {
 
 namespace {
 
-constexpr int kExtendThreads = 512;
+constexpr int kExtendThreads = 256;
 
 // Exclusive prefix sum over the block's threads, and the total.  int64: lengths are any int32 values.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total) {
@@ -79,7 +79,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total) {
 
 struct ExtendArgs {
   int batch, heads, bs, max_blocks, n_free;
-  int64_t n_blocks, n_rows;
+  int64_t n_blocks, n_rows, rows_each;  // rows of a block of the grid
   int32_t *table;
   const int32_t *lens, *grow, *free_blocks, *free_head;
   int32_t *lens_out, *granted, *free_head_out;
@@ -101,13 +101,15 @@ struct Grown {
 //
 // SLOTS: this block writes the slots and table entries of its equal share of the rows.  A few tokens per
 // sequence take one block that does both halves; for whole prompts every block of a large grid repeats
-// the scan (a microsecond) and writes its share, 8 bytes per (row, head), and STATE, the lengths and
-// counters, follows in a second launch: they may be updated in place, after every block has read them.
+// the scan (a microsecond) and writes its share, 8 bytes per (row, head).  STATE: the first block writes the
+// lengths and counters.  Where a large grid would update them in place, they follow in a launch of their
+// own, after every block has read them.
 //
 // A thread writes the slots of VEC neighbouring heads of a row at once, which differ by a block's tokens:
 // the row's look-ups, some 60 instructions, are what bounds this kernel before the stores do.
 template <bool SLOTS, bool STATE, int VEC>
 __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs a) {
+  const bool state = STATE && blockIdx.x == 0;
   __shared__ int64_t first_row[kExtendThreads + 1];
   __shared__ Grown grown[kExtendThreads];
   int64_t rows0 = 0, need0 = 0;  // sums before this chunk
@@ -116,23 +118,23 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t head = min(max((int64_t)*a.free_head, (int64_t)0), (int64_t)a.n_free);
-  const int64_t lo = a.n_rows * blockIdx.x / gridDim.x, hi = a.n_rows * (blockIdx.x + 1) / gridDim.x;
+  const int64_t lo = min(a.rows_each * blockIdx.x, a.n_rows), hi = min(lo + a.rows_each, a.n_rows);
   for (int b0 = 0; b0 < a.batch; b0 += kExtendThreads) {
     const int b = b0 + threadIdx.x;
     const bool in = b < a.batch;
-    const int64_t len = in ? max(a.lens[b], 0) : 0, add = in ? max(a.grow[b], 0) : 0;
-    const int64_t have = (len + a.bs - 1) / a.bs;
+    const int len = in ? max(a.lens[b], 0) : 0, add = in ? max(a.grow[b], 0) : 0;
+    const int have = len > 0 ? a.by_bs(len - 1) + 1 : 0;
     // the rows' offsets decide which sequences fit, so they come before the blocks' sum
     int64_t rows_total, need_total;
     const int64_t row = rows0 + block_scan(add, rows_total);
-    const bool fits = len + add <= most && row + add <= a.n_rows;
-    const int64_t need = in && fits ? (len + add + a.bs - 1) / a.bs - have : 0;
+    const bool fits = (int64_t)len + add <= most && row + add <= a.n_rows;
+    const int64_t need = in && fits && add > 0 ? a.by_bs(len + add - 1) + 1 - have : 0;
     const int64_t upto = need0 + block_scan(need, need_total);
     const bool ok = fits && (need == 0 || head + upto + need <= a.n_free);
-    if (STATE && in) {
+    if (state && in) {
       a.offsets[b] = row;
-      a.granted[b] = ok ? (int32_t)add : 0;
-      a.lens_out[b] = (int32_t)(ok ? len + add : len);
+      a.granted[b] = ok ? add : 0;
+      a.lens_out[b] = ok ? len + add : len;
       if (ok) taken += need;
     }
     if (SLOTS && rows0 < hi && rows0 + rows_total > lo) {
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
       first_row[threadIdx.x] = row;
       if (threadIdx.x == 0) first_row[count] = rows0 + rows_total;
       // a sequence that is not grown is never asked for its other values
-      grown[threadIdx.x] = Grown{(int)len, (int)have, (int)(ok ? head + upto : 0), ok && add > 0};
+      grown[threadIdx.x] = Grown{len, have, (int)(ok ? head + upto : 0), ok && add > 0};
       __syncthreads();
       const int64_t r0 = max(lo, rows0), r1 = min(hi, rows0 + rows_total);
       // rows x heads stays below 2^31 in a pass of this many rows
@@ -148,43 +150,57 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
       const int64_t pass = max((int64_t)1, (int64_t)(1 << 30) / parts);
       for (int64_t p0 = r0; p0 < r1; p0 += pass) {
         const int n = (int)(min(r1, p0 + pass) - p0) * parts;
-        int s = 0;  // sequence of the last row looked up: rows come in order
-        int64_t s_lo = 1, s_hi = 0;
-        for (int i = threadIdx.x; i < n; i += kExtendThreads) {
-          const int k = a.by_parts(i), h = (i - k * parts) * VEC;
-          const int64_t r = p0 + k;
-          if (r < s_lo || r >= s_hi) {
-            int u = 0, v = count;  // first_row[u] <= r < first_row[v]
-            while (v - u > 1) {
-              const int mid = (u + v) >> 1;
-              if (first_row[mid] <= r) u = mid;
-              else v = mid;
-            }
-            s = u;
-            s_lo = first_row[u];
-            s_hi = first_row[u + 1];
-          }
+        // block that group i (VEC heads of one row) of sequence s lies in, and then its slots
+        auto entry_of = [&](int i, int s, int64_t s_lo) {
           const Grown g = grown[s];
-          int64_t slot = -1;
-          if (g.ok) {
-            const int pos = g.before + (int)(r - s_lo), j = a.by_bs(pos), off = pos - j * a.bs;
-            int32_t *entry = a.table + (int64_t)(b0 + s) * a.max_blocks + j;
-            int e;
-            if (j >= g.have) {
-              e = __ldg(a.free_blocks + g.at + (j - g.have));
-              if (off == 0 && h == 0) *entry = e;  // a new block begins with a new row
-            } else {
-              e = *entry;
-            }
-            if (e >= 0 && e < a.n_blocks) slot = ((int64_t)e * a.heads + h) * a.bs + off;
-          }
-          const int64_t step = slot < 0 ? 0 : a.bs;
+          if (!g.ok) return -1;
+          const int j = a.by_bs(g.before + (int)(p0 + a.by_parts(i) - s_lo));
+          return j >= g.have ? __ldg(a.free_blocks + g.at + (j - g.have)) : a.table[(int64_t)(b0 + s) * a.max_blocks + j];
+        };
+        auto slots_of = [&](int i, int s, int64_t s_lo, int e) {
+          const Grown g = grown[s];
+          const int k = a.by_parts(i), h = (i - k * parts) * VEC;
+          const int pos = g.before + (int)(p0 + k - s_lo), j = a.by_bs(pos), off = pos - j * a.bs;
+          if (g.ok && j >= g.have && off == 0 && h == 0)  // a new block begins with a new row
+            a.table[(int64_t)(b0 + s) * a.max_blocks + j] = e;
+          const bool in = g.ok && e >= 0 && e < a.n_blocks;
+          const int64_t slot = in ? ((int64_t)e * a.heads + h) * a.bs + off : -1, step = in ? a.bs : 0;
           if constexpr (VEC == 1) {
             a.slots[p0 * parts + i] = slot;
           } else {
             longlong2 *to = reinterpret_cast<longlong2 *>(a.slots) + (p0 * parts + i) * (VEC / 2);
 #pragma unroll
             for (int x = 0; x < VEC / 2; ++x) to[x] = make_longlong2(slot + 2 * x * step, slot + (2 * x + 1) * step);
+          }
+        };
+        auto find = [&](int64_t r) {  // first_row[u] <= r < first_row[u + 1]
+          int u = 0, v = count;
+          while (v - u > 1) {
+            const int mid = (u + v) >> 1;
+            if (first_row[mid] <= r) u = mid;
+            else v = mid;
+          }
+          return u;
+        };
+        // where prompts are long, each sequence in turn, four look-ups in flight; else a search for each group
+        const int s0 = find(p0), s1 = find(min(r1, p0 + pass) - 1);
+        if (s1 - s0 < n / (4 * kExtendThreads)) {
+          for (int s = s0; s <= s1; ++s) {
+            const int64_t s_lo = first_row[s];
+            const int from = (int)(max(s_lo, p0) - p0) * parts, to = (int)min((first_row[s + 1] - p0) * parts, (int64_t)n);
+            for (int i = from + threadIdx.x; i < to; i += 4 * kExtendThreads) {
+              int e[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) e[x] = i + x * kExtendThreads < to ? entry_of(i + x * kExtendThreads, s, s_lo) : -1;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (i + x * kExtendThreads < to) slots_of(i + x * kExtendThreads, s, s_lo, e[x]);
+            }
+          }
+        } else {
+          for (int i = threadIdx.x; i < n; i += kExtendThreads) {
+            const int s = find(p0 + a.by_parts(i));
+            slots_of(i, s, first_row[s], entry_of(i, s, first_row[s]));
           }
         }
       }
@@ -195,7 +211,7 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
   }
   if (SLOTS)  // behind the last sequence
     for (int64_t i = max(lo, rows0) * a.heads + threadIdx.x; i < hi * a.heads; i += kExtendThreads) a.slots[i] = -1;
-  if (STATE) {
+  if (state) {
     int64_t total;
     block_scan(taken, total);
     if (threadIdx.x == 0) {
@@ -206,7 +222,8 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
 }
 
 // Slots, in units of VEC, up to which one block does the whole call.
-constexpr int64_t kExtendOneBlock = 4096;
+constexpr int64_t kExtendOneBlock = 2048;
+constexpr int kExtendBlocksPerSm = 6;
 
 struct AppendArgs {
   int batch, heads, bs, max_blocks, d;
@@ -348,16 +365,21 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
 }
 
 template <int VEC>
-cudaError_t launch_extend(const ExtendArgs &a, int64_t n_slots, int device, cudaStream_t st) {
-  if (n_slots <= kExtendOneBlock * VEC) {
+cudaError_t launch_extend(ExtendArgs a, int64_t n_slots, int device, cudaStream_t st) {
+  const int64_t want = n_slots <= kExtendOneBlock * VEC ? 1 : n_slots / (4 * VEC * kExtendThreads) + 1;
+  const int64_t most = kExtendBlocksPerSm * (int64_t)tq_device_sms(device);
+  const unsigned grid = (unsigned)(want < most ? want : most);
+  a.rows_each = (a.n_rows + grid - 1) / grid;
+  const bool in_place = a.lens_out == a.lens || a.granted == a.grow || a.free_head_out == a.free_head;
+  if (want == 1 || !in_place) {
     tq_prof_begin(TQK_PAGE_EXTEND, st);
-    const cudaError_t e = tq_launch_dependent(page_extend_kernel<true, true, VEC>, dim3(1), kExtendThreads, 0, st, a);
+    const cudaError_t e =
+        tq_launch_dependent(page_extend_kernel<true, true, VEC>, dim3(grid), kExtendThreads, 0, st, a);
     tq_prof_end(TQK_PAGE_EXTEND, st);
     return e;
   }
-  const int64_t want = n_slots / (4 * VEC * kExtendThreads) + 1, most = 4 * (int64_t)tq_device_sms(device);
   tq_prof_begin(TQK_PAGE_SLOTS, st);
-  cudaError_t e = tq_launch_dependent(page_extend_kernel<true, false, VEC>, dim3((unsigned)(want < most ? want : most)), kExtendThreads, 0, st, a);
+  cudaError_t e = tq_launch_dependent(page_extend_kernel<true, false, VEC>, dim3(grid), kExtendThreads, 0, st, a);
   tq_prof_end(TQK_PAGE_SLOTS, st);
   if (e != cudaSuccess) return e;
   tq_prof_begin(TQK_PAGE_EXTEND, st);
@@ -390,7 +412,7 @@ extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_le
   if (st != TQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ExtendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, n_free, pages->n_blocks,
-               n_slots / pages->n_kv_heads, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
+               n_slots / pages->n_kv_heads, 0, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
                seq_lens_out, granted, free_head_out, row_offsets, new_slots, FastDiv(), FastDiv(pages->block_size)};
   const int vec = !tq_aligned(new_slots, 16) ? 1 : pages->n_kv_heads % 4 == 0 ? 4 : pages->n_kv_heads % 2 == 0 ? 2 : 1;
   a.by_parts = FastDiv(pages->n_kv_heads / vec);
