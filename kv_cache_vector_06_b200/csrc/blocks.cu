@@ -112,28 +112,33 @@ struct Scorer<float, D, WIDE> {
   static constexpr int kEach = 8 / kAt;             // blocks of a lane
   static constexpr int kVec = D == 256 ? 2 : 1;
   static constexpr int kHeads = WIDE ? 16 : 8;
-  float4 q[kHeads][kVec];
+  static constexpr bool kQInRegs = kHeads * kVec <= 16;  // else four heads at a time, from the cache
+  float4 q[kQInRegs ? kHeads : 4][kVec];
 
   static __device__ __forceinline__ int chunk(int, int ch) { return ch; }
-  __device__ __forceinline__ void ask(const BlockScoreArgs &a, int64_t row, int lane) {
+  __device__ __forceinline__ void load(const BlockScoreArgs &a, int64_t row, int h0, int lane) {
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
+    for (int h = 0; h < (kQInRegs ? kHeads : 4); ++h)
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         const int ch = lane % kLanes + 32 * v;
         q[h][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h < a.group && 4 * ch < a.d)
-          q[h][v] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + (row * a.group + h) * a.d) + ch);
+        if (h0 + h < a.group && 4 * ch < a.d)
+          q[h][v] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + (row * a.group + h0 + h) * a.d) + ch);
       }
+  }
+  __device__ __forceinline__ void ask(const BlockScoreArgs &a, int64_t row, int lane) {
+    if constexpr (kQInRegs) load(a, row, 0, lane);
   }
   __device__ __forceinline__ void prepare() {}
   static __device__ __forceinline__ float pick(float x, float lo, float hi, float s) { return fmaf(x, x >= 0.f ? hi : lo, s); }
-  __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t, unsigned lower, unsigned upper, int lane, int &k) {
+  __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t row, unsigned lower, unsigned upper, int lane, int &k) {
     const int v = lane % kLanes;
     float best = -INFINITY;
 #pragma unroll
     for (int h0 = 0; h0 < kHeads; h0 += 4) {
       if (h0 >= a.group) break;
+      if constexpr (!kQInRegs) load(a, row, h0, lane);
       float s[4 * kEach];  // [head][block]
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -145,7 +150,7 @@ struct Scorer<float, D, WIDE> {
           lds128(u, upper + i * kAt * S::kRow + 16 * (lane + 32 * w));
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const float4 x = q[h0 + h][w];
+            const float4 x = q[(kQInRegs ? h0 : 0) + h][w];
             t[h] = pick(x.x, __uint_as_float(l[0]), __uint_as_float(u[0]), t[h]);
             t[h] = pick(x.y, __uint_as_float(l[1]), __uint_as_float(u[1]), t[h]);
             t[h] = pick(x.z, __uint_as_float(l[2]), __uint_as_float(u[2]), t[h]);

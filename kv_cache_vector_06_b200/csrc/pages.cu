@@ -150,27 +150,22 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
       const int64_t pass = max((int64_t)1, (int64_t)(1 << 30) / parts);
       for (int64_t p0 = r0; p0 < r1; p0 += pass) {
         const int n = (int)(min(r1, p0 + pass) - p0) * parts;
-        // block that group i (VEC heads of one row) of sequence s lies in, and then its slots
-        auto entry_of = [&](int i, int s, int64_t s_lo) {
-          const Grown g = grown[s];
-          if (!g.ok) return -1;
-          const int j = a.by_bs(g.before + (int)(p0 + a.by_parts(i) - s_lo));
-          return j >= g.have ? __ldg(a.free_blocks + g.at + (j - g.have)) : a.table[(int64_t)(b0 + s) * a.max_blocks + j];
+        // entry of a sequence's block j, and the slots of heads h .. h + VEC - 1 of token `off` of that block
+        auto entry_of = [&](const Grown &g, const int32_t *table, int j) {
+          return !g.ok ? -1 : j >= g.have ? __ldg(a.free_blocks + g.at + (j - g.have)) : table[j];
         };
-        auto slots_of = [&](int i, int s, int64_t s_lo, int e) {
-          const Grown g = grown[s];
-          const int k = a.by_parts(i), h = (i - k * parts) * VEC;
-          const int pos = g.before + (int)(p0 + k - s_lo), j = a.by_bs(pos), off = pos - j * a.bs;
-          if (g.ok && j >= g.have && off == 0 && h == 0)  // a new block begins with a new row
-            a.table[(int64_t)(b0 + s) * a.max_blocks + j] = e;
-          const bool in = g.ok && e >= 0 && e < a.n_blocks;
-          const int64_t slot = in ? ((int64_t)e * a.heads + h) * a.bs + off : -1, step = in ? a.bs : 0;
+        auto slots_of = [&](const Grown &g, int32_t *table, int j, int off, int h, int64_t *to, int e) {
+          if (off == 0 && h == 0 && g.ok && j >= g.have) table[j] = e;  // a new block begins with a new row
+          const bool in = e >= 0 && e < a.n_blocks;
+          const int64_t slot = in ? (int64_t)(e * a.heads + h) * a.bs + off : -1, step = in ? a.bs : 0;
           if constexpr (VEC == 1) {
-            a.slots[p0 * parts + i] = slot;
+            *to = slot;
+          } else if constexpr (VEC == 2) {
+            *reinterpret_cast<longlong2 *>(to) = make_longlong2(slot, slot + step);
           } else {
-            longlong2 *to = reinterpret_cast<longlong2 *>(a.slots) + (p0 * parts + i) * (VEC / 2);
-#pragma unroll
-            for (int x = 0; x < VEC / 2; ++x) to[x] = make_longlong2(slot + 2 * x * step, slot + (2 * x + 1) * step);
+            asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};\n" ::"l"(to), "l"(slot), "l"(slot + step), "l"(slot + 2 * step),
+                         "l"(slot + 3 * step)
+                         : "memory");
           }
         };
         auto find = [&](int64_t r) {  // first_row[u] <= r < first_row[u + 1]
@@ -182,25 +177,42 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
           }
           return u;
         };
-        // where prompts are long, each sequence in turn, four look-ups in flight; else a search for each group
-        const int s0 = find(p0), s1 = find(min(r1, p0 + pass) - 1);
-        if (s1 - s0 < n / (4 * kExtendThreads)) {
-          for (int s = s0; s <= s1; ++s) {
-            const int64_t s_lo = first_row[s];
-            const int from = (int)(max(s_lo, p0) - p0) * parts, to = (int)min((first_row[s + 1] - p0) * parts, (int64_t)n);
-            for (int i = from + threadIdx.x; i < to; i += 4 * kExtendThreads) {
-              int e[4];
+        // where prompts are long, each sequence in turn, a thread keeping its heads and taking four rows at a
+        // time, mostly of one block, whose entry is asked for one turn ahead; else a search for each row
+        const int s0 = find(p0), s1 = find(min(r1, p0 + pass) - 1), at_once = kExtendThreads / parts;
+        if (at_once > 0 && s1 - s0 < n / (4 * kExtendThreads)) {
+          const int sub = a.by_parts(threadIdx.x), h = (threadIdx.x - sub * parts) * VEC;
+          for (int s = s0; s <= s1 && sub < at_once; ++s) {
+            const int64_t s_lo = first_row[s], from = max(s_lo, p0);
+            const int rows = (int)(min(first_row[s + 1], min(r1, p0 + pass)) - from);
+            const Grown g = grown[s];
+            const int pos = g.before + (int)(from - s_lo);
+            int32_t *table = a.table + (int64_t)(b0 + s) * a.max_blocks;
+            int64_t *to = a.slots + ((from + 4 * sub) * a.heads + h);
+            int j = a.by_bs(pos + 4 * sub), next = 4 * sub < rows ? entry_of(g, table, j) : -1;
+            for (int i = 4 * sub; i < rows; i += 4 * at_once) {
+              int e = next, now = j, off = pos + i - j * a.bs;
+              j = a.by_bs(pos + i + 4 * at_once);
+              if (i + 4 * at_once < rows) next = entry_of(g, table, j);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) e[x] = i + x * kExtendThreads < to ? entry_of(i + x * kExtendThreads, s, s_lo) : -1;
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (i + x * kExtendThreads < to) slots_of(i + x * kExtendThreads, s, s_lo, e[x]);
+              for (int x = 0; x < 4; ++x) {
+                if (i + x >= rows) break;
+                if (off == a.bs) {
+                  off = 0;
+                  e = entry_of(g, table, ++now);
+                }
+                slots_of(g, table, now, off++, h, to + x * a.heads, e);
+              }
+              to += (int64_t)4 * at_once * a.heads;
             }
           }
         } else {
           for (int i = threadIdx.x; i < n; i += kExtendThreads) {
-            const int s = find(p0 + a.by_parts(i));
-            slots_of(i, s, first_row[s], entry_of(i, s, first_row[s]));
+            const int k = a.by_parts(i), s = find(p0 + k), h = (i - k * parts) * VEC;
+            const Grown g = grown[s];
+            const int pos = g.before + (int)(p0 + k - first_row[s]), j = a.by_bs(pos);
+            int32_t *table = a.table + (int64_t)(b0 + s) * a.max_blocks;
+            slots_of(g, table, j, pos - j * a.bs, h, a.slots + ((p0 + k) * a.heads + h), entry_of(g, table, j));
           }
         }
       }
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
 
 // Slots, in units of VEC, up to which one block does the whole call.
 constexpr int64_t kExtendOneBlock = 2048;
-constexpr int kExtendBlocksPerSm = 6;
+constexpr int kExtendBlocksPerSm = 4;
 
 struct AppendArgs {
   int batch, heads, bs, max_blocks, d;
@@ -414,7 +426,9 @@ extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_le
   ExtendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, n_free, pages->n_blocks,
                n_slots / pages->n_kv_heads, 0, pages->block_table, seq_lens, new_lens, free_blocks, free_head,
                seq_lens_out, granted, free_head_out, row_offsets, new_slots, FastDiv(), FastDiv(pages->block_size)};
-  const int vec = !tq_aligned(new_slots, 16) ? 1 : pages->n_kv_heads % 4 == 0 ? 4 : pages->n_kv_heads % 2 == 0 ? 2 : 1;
+  const int vec = pages->n_kv_heads % 4 == 0 && tq_aligned(new_slots, 32)   ? 4
+                  : pages->n_kv_heads % 2 == 0 && tq_aligned(new_slots, 16) ? 2
+                                                                            : 1;
   a.by_parts = FastDiv(pages->n_kv_heads / vec);
   cudaError_t e = vec == 4 ? launch_extend<4>(a, n_slots, pages->device, s) : vec == 2 ? launch_extend<2>(a, n_slots, pages->device, s) : launch_extend<1>(a, n_slots, pages->device, s);
   return tq_cuda_check(e, "page extend launch");
