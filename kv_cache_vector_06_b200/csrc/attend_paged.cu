@@ -75,7 +75,7 @@ struct Stream {
     constexpr int kT = S::kTok / 8;
     const int c = lane & 3, r = lane >> 2;
     // chunk 4 kg + c of token r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
-    const unsigned at[2] = {r * S::kRow + 16 * key_chunk(r, c), r * S::kRow + 16 * key_chunk(r, 4 + c)};
+    const unsigned at[2] = {(unsigned)(r * S::kRow + 16 * key_chunk(r, c)), (unsigned)(r * S::kRow + 16 * key_chunk(r, 4 + c))};
     float s[kBf ? kT : 2][4];  // fp32: two sums, of every other group, so that the products wait less for one another
 #pragma unroll
     for (int t = 0; t < (kBf ? kT : 2); ++t)

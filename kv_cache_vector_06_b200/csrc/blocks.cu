@@ -58,7 +58,7 @@ struct Scorer {
   __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t row, unsigned lower, unsigned upper, int lane, int &k) {
     const int c = lane & 3, r = lane >> 2;
     // chunk 4 kg + c of block r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
-    const unsigned at[2] = {r * S::kRow + 16 * key_chunk(r, c), r * S::kRow + 16 * key_chunk(r, 4 + c)};
+    const unsigned at[2] = {(unsigned)(r * S::kRow + 16 * key_chunk(r, c)), (unsigned)(r * S::kRow + 16 * key_chunk(r, 4 + c))};
     float s[2][kT][4];
 #pragma unroll
     for (int x = 0; x < 8 * kT; ++x) s[x / (4 * kT)][x / 4 % kT][x % 4] = 0.f;
@@ -302,7 +302,6 @@ struct SelectArgs {
   int32_t *sel_table, *sel_lens;
 };
 
-constexpr int kSelectThreads = 512;
 constexpr int kSelectList = 2048;  // keys of one leading digit that are put aside
 
 // A float's order as an unsigned integer: larger floats have larger keys, -0 and +0 the same one, and
@@ -313,8 +312,9 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 }
 
 // Exclusive prefix sums of two counts (each below 2^16 per block) over the block's threads, and their totals.
+template <int THREADS>
 __device__ __forceinline__ void block_scan(int a, int b, int &ea, int &eb, int &ta, int &tb) {
-  __shared__ uint32_t w[kSelectThreads / 32];
+  __shared__ uint32_t w[THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t v = (uint32_t)a | ((uint32_t)b << 16);
   uint32_t s = v;
@@ -327,7 +327,7 @@ __device__ __forceinline__ void block_scan(int a, int b, int &ea, int &eb, int &
   __syncthreads();
   uint32_t p = 0, t = 0;
 #pragma unroll
-  for (int i = 0; i < kSelectThreads / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     const uint32_t x = w[i];
     if (i < warp) p += x;
     t += x;
@@ -342,17 +342,24 @@ __device__ __forceinline__ void block_scan(int a, int b, int &ea, int &eb, int &
 
 // The 2048 counts of `hist`, largest digit first, cut where `need` of them are passed: the digit, and how many
 // of its keys are still needed.  Leaves the counts at zero.
+template <int THREADS>
 __device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &rest) {
-  __shared__ int wsum[kSelectThreads / 32];
+  __shared__ int wsum[THREADS / 32];
   __shared__ int found, left;
-  constexpr int kPer = 2048 / kSelectThreads;
+  constexpr int kPer = 2048 / THREADS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = 2047 - kPer * threadIdx.x;
-  int4 *mine = reinterpret_cast<int4 *>(hist + top - 3);
-  static_assert(kPer == 4, "one int4 of counts per thread");
-  const int4 v = *mine;
-  *mine = make_int4(0, 0, 0, 0);
-  const int cnt[4] = {v.w, v.z, v.y, v.x};
-  const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+  int cnt[kPer], sum = 0;  // from the thread's largest digit down
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {
+    int4 *mine = reinterpret_cast<int4 *>(hist + top - 3 - i);
+    const int4 v = *mine;
+    *mine = make_int4(0, 0, 0, 0);
+    cnt[i] = v.w;
+    cnt[i + 1] = v.z;
+    cnt[i + 2] = v.y;
+    cnt[i + 3] = v.x;
+    sum += v.x + v.y + v.z + v.w;
+  }
   int s = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -363,13 +370,13 @@ __device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &
   __syncthreads();
   int before = s - sum;
 #pragma unroll
-  for (int i = 0; i < kSelectThreads / 32; ++i)
+  for (int i = 0; i < THREADS / 32; ++i)
     if (i < warp) before += wsum[i];
   int r = need - before;
   if (r > 0 && r <= sum) {
     int i = 0;
 #pragma unroll
-    for (int x = 0; x < 3; ++x)
+    for (int x = 0; x < kPer - 1; ++x)
       if (i == x && r > cnt[x]) {
         r -= cnt[x];
         ++i;
@@ -386,17 +393,19 @@ __device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &
 // counts of its digits (11, 11 and 10 bits), the leading one over all keys; the keys that share it are then
 // put aside, a few hundred of them where scores spread, and the other digits are found among those.  One
 // pass in index order writes the blocks above that key and the first ones at it.  Each thread holds PER
-// consecutive keys, so that index order is thread order; rows longer than a block's PER * 512 keys go
+// consecutive keys, so that index order is thread order; rows longer than a block's PER * THREADS keys go
 // through in chunks, read again for each pass, and so do those where a digit's keys outgrow the list.
-template <int PER>
-__global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArgs a) {
-  constexpr int kChunk = PER * kSelectThreads;
+// Latency bounds it: a dozen barriers and scans.  Tables of up to 2048 blocks take 256 threads (64 sequences x
+// 8 heads of 64 .. 2048 blocks: 8.7 us per call in a row of calls, 10.8 with 512, 12.2 with 128), longer ones
+// 512.  The next kernel is let in late: its waiting blocks crowd this one's onto fewer SMs (11.1 us).
+template <int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) select_blocks_kernel(SelectArgs a) {
+  constexpr int kChunk = PER * THREADS;
   __shared__ __align__(16) int hist[2048];
   __shared__ uint32_t list[kSelectList];
   __shared__ int listed;
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 2048 / kSelectThreads; ++i) hist[threadIdx.x + i * kSelectThreads] = 0;
+  for (int i = 0; i < 2048 / THREADS; ++i) hist[threadIdx.x + i * THREADS] = 0;
   if (threadIdx.x == 0) listed = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
@@ -410,13 +419,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
   const float *scores = a.scores + row * a.max_blocks;
   const int kept = n < a.keep ? n : a.keep;
   if (threadIdx.x == 0) a.sel_lens[row] = n > 0 ? (kept - 1) * a.bs + (len - (n - 1) * a.bs) : 0;
-  for (int i = kept + threadIdx.x; i < a.keep; i += kSelectThreads) out[i] = -1;
+  for (int i = kept + threadIdx.x; i < a.keep; i += THREADS) out[i] = -1;
   auto store = [&](int i, int j) {
     const int e = table[j];
     out[i] = e >= 0 && e < a.n_blocks ? e * a.heads + h : -1;
   };
   if (n <= a.keep) {
-    for (int j = threadIdx.x; j < n; j += kSelectThreads) store(j, j);
+    for (int j = threadIdx.x; j < n; j += THREADS) store(j, j);
     return;
   }
   const int lo = a.first, hi = n - a.last;  // candidates [lo, hi); the others are always chosen
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
         if (k[i] != 0) atomicAdd(&hist[k[i] >> 21], 1);
     }
     __syncthreads();
-    cut_digit(hist, need, digit, equal);
+    cut_digit<THREADS>(hist, need, digit, equal);
     key = (uint32_t)digit << 21;
     for (int j0 = 0; j0 < n; j0 += kChunk) {
       if (!once) load(j0);
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
       const int shift = pass ? 0 : 10, above = pass ? 10 : 21;
       const uint32_t mask = pass ? 1023u : 2047u;
       if (count <= kSelectList) {
-        for (int i = threadIdx.x; i < count; i += kSelectThreads)
+        for (int i = threadIdx.x; i < count; i += THREADS)
           if (((list[i] ^ key) >> above) == 0) atomicAdd(&hist[(list[i] >> shift) & mask], 1);
       } else {
         for (int j0 = 0; j0 < n; j0 += kChunk) {
@@ -486,10 +495,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
         }
       }
       __syncthreads();
-      cut_digit(hist, equal, digit, equal);
+      cut_digit<THREADS>(hist, equal, digit, equal);
       key |= (uint32_t)digit << shift;
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   int at = 0, seen = 0;  // blocks written, blocks at `key` passed, before this chunk
   for (int j0 = 0; j0 < n; j0 += kChunk) {
     if (!once) load(j0);
@@ -506,7 +516,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_blocks_kernel(SelectArg
         if (j + i < n && (j + i < lo || j + i >= hi)) above |= 1u << i;
     }
     int ea, eb, ta, tb;
-    block_scan(__popc(above), __popc(ties), ea, eb, ta, tb);
+    block_scan<THREADS>(__popc(above), __popc(ties), ea, eb, ta, tb);
     // of the row's ties the first `equal` are taken: so many of this thread's
     const int first = seen + eb;
     int p = at + ea + min(first, equal) - min(seen, equal);
@@ -580,8 +590,8 @@ extern "C" tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_
                pages->n_blocks, pages->block_table, seq_lens, scores, sel_table, sel_lens};
   tq_prof_begin(TQK_SELECT_BLOCKS, s);
   const unsigned grid = (unsigned)(pages->batch * pages->n_kv_heads);
-  const cudaError_t e = tq_launch_dependent(pages->max_blocks <= 4 * kSelectThreads ? select_blocks_kernel<4> : select_blocks_kernel<16>,
-                                            dim3(grid), kSelectThreads, 0, s, a);
+  const cudaError_t e = pages->max_blocks <= 2048 ? tq_launch_dependent(select_blocks_kernel<256, 8>, dim3(grid), 256, 0, s, a)
+                                                  : tq_launch_dependent(select_blocks_kernel<512, 16>, dim3(grid), 512, 0, s, a);
   tq_prof_end(TQK_SELECT_BLOCKS, s);
   return tq_cuda_check(e, "block selection launch");
 }

@@ -464,10 +464,12 @@ def search_topk(ctx: Context, q: torch.Tensor, db: Packed, k: int, n: int = None
     return out_scores, out_idx
 
 
+# the current stream's handle without a Stream object around it (a microsecond per call), where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
 def _raw_stream(device: int, stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 class Pages:
