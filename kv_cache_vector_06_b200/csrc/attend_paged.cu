@@ -12,6 +12,7 @@
 // warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
 // A row that falls to several workers leaves pieces (m, l, o) in the workspace, joined by a second
 // kernel.
+#include <algorithm>
 #include "paged_device.cuh"
 
 namespace {
@@ -24,14 +25,18 @@ struct PagedArgs {
   const void *q, *k, *v;
   void *out;
   FastDiv by_bs;
-  int4 *owner;   // [workers]: row whose pieces this worker begins, their number (0: none), slots from one to the next
+  int2 *owner;   // [rows]: slot of the first piece, and pieces (0: the output is written), negated where they lie a warp apart
   float *piece;  // [workers][2][piece_floats]: [group][d] o, then [group] m, [group] l of each
 };
 
 // What a row costs a worker beside its steps (its queries, its first loads, the joining of the warps), in
-// steps of the worker: a batch of 7 rows x 4 heads of 1 to 9999 tokens took
-// TODO
-constexpr int kTeamRowCost = 8, kSoloRowCost = 2;
+// steps of the worker: as long as 64 KB (a block) or 16 KB (a warp) of the cache take it.  Without it a block
+// that drew several short rows ended last: 7 sequences of 1 to 9999 tokens x 4 heads took 47 us, with it 35.
+template <int D>
+constexpr int kTeamRowCost = 1024 / D;
+template <int D>
+constexpr int kSoloRowCost = 256 / D;
+
 // Floats of one piece, a multiple of four.
 __host__ __device__ __forceinline__ int piece_floats(int group, int d) { return (group * (d + 2) + 3) & ~3; }
 
@@ -256,9 +261,10 @@ struct Stream {
 };
 
 template <typename T, int D, bool WIDE, int PARTS, typename O>
-__global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kernel(PagedArgs a) {
+__global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) attend_paged_kernel(PagedArgs a) {
   using S = Shape<T, D>;
   using St = Stream<T, D, WIDE, PARTS>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Place place[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
@@ -267,19 +273,18 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-  StepScan scan;
+  StepScan<kWarps> scan;
   scan.run(a.lens, a.batch, a.heads, a.max_len, S::kTok);
   // ---- workers
   const int64_t rows = (int64_t)a.batch * a.heads;
   const bool solo = rows >= (int64_t)gridDim.x && scan.total < 8 * rows;
-  const int team = solo ? 1 : kWarps, extra = solo ? kSoloRowCost : kTeamRowCost;
+  const int team = solo ? 1 : kWarps, extra = solo ? kSoloRowCost<D> : kTeamRowCost<D>;
   const int64_t workers = max((int64_t)1, min((int64_t)gridDim.x * (solo ? kWarps : 1), scan.total / (solo ? 1 : kWarps)));
   const Deal deal(scan.total + rows * extra, workers);
   for (int w = 0; w < kWarps; w += team) {
     const int64_t id = solo ? (int64_t)blockIdx.x * kWarps + w : (int64_t)blockIdx.x;
     if (id < workers) find_unit(scan, deal.begin(id), extra, a.lens, a.max_len, S::kTok, place[w]);
   }
-  if (lane == 0) a.owner[blockIdx.x * kWarps + warp] = make_int4(0, 0, 0, 0);
   __syncthreads();
   const int lead = solo ? warp : 0;  // first warp of the team
   const int slot0 = blockIdx.x * kWarps + lead;
@@ -451,93 +456,79 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) attend_paged_kern
       }
       __syncthreads();
     }
-    if (starts && !ends && rank == 0 && lane == 0) {
+    if (starts && rank == 0 && lane == 0) {
       // the row's last step decides how many workers hold pieces of it
-      const int64_t to = deal.owner(pos - unit + extra + steps - 1);
-      a.owner[slot0] = make_int4((int)row, (int)(to - id + 1), solo ? 1 : kWarps, 0);
+      const int n = done ? 0 : (int)(deal.owner(pos - unit + extra + steps - 1) - id) + 1;
+      a.owner[row] = make_int2(slot0, solo ? -n : n);
     }
     go_on();
   }
 }
 
-// Joins the pieces of rows that several workers shared: block x, the rows that block x of the kernel above
-// began.  Threads hold four channels of one head each; as many groups of them as the block has room for
-// take pieces in turn.  Latency-bound (a few hundred KB in all): four pieces in flight per thread.
+// Joins the pieces of rows that several workers shared: blocks (x, y), rows x, x + gridDim.x, ..., vectors of
+// four channels from y * vecs on.  A block holds as many groups of `vecs` threads as it has room for, which
+// take pieces in turn, four in flight per thread, and meet in shared memory.  Latency bounds it (a few hundred
+// KB in all): with few rows, of many pieces each, the host cuts them into small ranges of vectors (one row of
+// 296 pieces, 8 heads of 128 channels: 70 us in one range).
 constexpr int kMergeThreads = 256;
 template <typename O>
-__global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(PagedArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(PagedArgs a, int warps, int vecs) {
   __shared__ float4 so[kMergeThreads];
-  __shared__ float sm[kMergeThreads], sl[kMergeThreads];
-  const int g = a.group, vecs = g * a.d / 4, tid = threadIdx.x;
-  const int groups = vecs < kMergeThreads ? kMergeThreads / vecs : 1;
+  __shared__ float2 ml[kMergeThreads];
+  const int g = a.group, tid = threadIdx.x, groups = kMergeThreads / vecs, grp = tid / vecs;
+  const int v = blockIdx.y * vecs + tid - grp * vecs;
+  const bool on = grp < groups && 4 * v < g * a.d;
+  const int hd = on ? 4 * v / a.d : 0;
   const int64_t stride = piece_floats(g, a.d);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  int4 own[kWarps];
+  for (int64_t row = blockIdx.x; row < (int64_t)a.batch * a.heads; row += gridDim.x) {
+    const int2 own = a.owner[row];
+    if (own.y == 0) continue;
+    const int n = abs(own.y), apart = own.y < 0 ? 1 : warps;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](float pm, float pl, const float4 &po) {
+      if (pm == -INFINITY) return;
+      const float to = fmaxf(m, pm), f0 = exp2a(m - to), f1 = exp2a(pm - to);
+      m = to;
+      l = l * f0 + pl * f1;
+      o.x = o.x * f0 + po.x * f1;
+      o.y = o.y * f0 + po.y * f1;
+      o.z = o.z * f0 + po.z * f1;
+      o.w = o.w * f0 + po.w * f1;
+    };
+    for (int p0 = grp; on && p0 < n; p0 += 4 * groups) {
+      float pm[4], pl[4];
+      float4 po[4];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) own[w] = a.owner[blockIdx.x * kWarps + w];
-#pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    const int n = own[w].y;
-    if (n == 0) continue;
-    const float *base = a.piece + (int64_t)(blockIdx.x * kWarps + w) * 2 * stride;
-    for (int v0 = 0; v0 < vecs; v0 += kMergeThreads) {
-      const int grp = vecs < kMergeThreads ? tid / vecs : 0, v = v0 + tid - grp * vecs;
-      const bool on = grp < groups && v < vecs;
-      const int hd = on ? 4 * v / a.d : 0;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p0 = grp; on && p0 < n; p0 += 4 * groups) {
-        float pm[4], pl[4];
-        float4 po[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = p0 + i * groups;
-          pm[i] = -INFINITY;
-          if (p < n) {
-            const float *piece = base + ((int64_t)p * own[w].z * 2 + (p == 0 ? 1 : 0)) * stride;
-            pm[i] = piece[g * a.d + hd];
-            pl[i] = piece[g * a.d + g + hd];
-            po[i] = *reinterpret_cast<const float4 *>(piece + 4 * v);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (pm[i] == -INFINITY) continue;
-          const float to = fmaxf(m, pm[i]), f0 = exp2a(m - to), f1 = exp2a(pm[i] - to);
-          m = to;
-          l = l * f0 + pl[i] * f1;
-          o.x = o.x * f0 + po[i].x * f1;
-          o.y = o.y * f0 + po[i].y * f1;
-          o.z = o.z * f0 + po[i].z * f1;
-          o.w = o.w * f0 + po[i].w * f1;
+      for (int i = 0; i < 4; ++i) {
+        const int p = p0 + i * groups;
+        pm[i] = -INFINITY;
+        if (p < n) {
+          // a worker's two pieces: of a row that began before it, and of the row that it begins
+          const float *piece = a.piece + ((int64_t)(own.x + p * apart) * 2 + (p == 0 ? 1 : 0)) * stride;
+          pm[i] = piece[g * a.d + hd];
+          pl[i] = piece[g * a.d + g + hd];
+          po[i] = reinterpret_cast<const float4 *>(piece)[v];
         }
       }
-      if (groups > 1) {
-        sm[tid] = m;
-        sl[tid] = l;
-        so[tid] = o;
-        __syncthreads();
-        for (int i = 1; grp == 0 && on && i < groups; ++i) {
-          const float im = sm[tid + i * vecs];
-          if (im == -INFINITY) continue;
-          const float4 io = so[tid + i * vecs];
-          const float to = fmaxf(m, im), f0 = exp2a(m - to), f1 = exp2a(im - to);
-          m = to;
-          l = l * f0 + sl[tid + i * vecs] * f1;
-          o.x = o.x * f0 + io.x * f1;
-          o.y = o.y * f0 + io.y * f1;
-          o.z = o.z * f0 + io.z * f1;
-          o.w = o.w * f0 + io.w * f1;
-        }
-        __syncthreads();
-      }
-      if (grp == 0 && on) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        O *out = static_cast<O *>(a.out) + (int64_t)own[w].x * g * a.d + 4 * v;
-        store2(out, o.x * inv, o.y * inv);
-        store2(out + 2, o.z * inv, o.w * inv);
-      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) join(pm[i], pl[i], po[i]);
+    }
+    if (groups > 1) {
+      so[tid] = o;
+      ml[tid] = make_float2(m, l);
+      __syncthreads();
+      if (grp == 0 && on)
+        for (int i = 1; i < groups; ++i) join(ml[tid + i * vecs].x, ml[tid + i * vecs].y, so[tid + i * vecs]);
+      __syncthreads();
+    }
+    if (grp == 0 && on) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      O *out = static_cast<O *>(a.out) + row * g * a.d + 4 * v;
+      store2(out, o.x * inv, o.y * inv);
+      store2(out + 2, o.z * inv, o.w * inv);
     }
   }
 }
@@ -557,40 +548,48 @@ tq_status check_attend(const tq_pages *pages, int32_t max_seq_len, int32_t n_q_h
   return TQ_OK;
 }
 
-// Blocks of the attention kernel: as many as fit on the GPU at once, fewer where the rows could not give
-// each a step per warp.  The same for both cache types (8 tokens per step counted for bf16 too), so that
-// one workspace size serves them.
-int attend_grid(const tq_pages &p, int32_t max_seq_len, int32_t d) {
-  const int occ = d <= 64 ? Shape<float, 64>::kOcc : d <= 128 ? Shape<float, 128>::kOcc : Shape<float, 256>::kOcc;
-  const int64_t steps = (int64_t)p.batch * p.n_kv_heads * (max_seq_len <= 8 ? 1 : (max_seq_len - 1) / 8 + 1);
-  const int64_t want = (steps + kWarps - 1) / kWarps, most = (int64_t)occ * tq_device_sms(p.device);
-  return (int)(want < 1 ? 1 : want < most ? want : most);
+// The workspace: the rows' owners, and two pieces for each warp of the largest grid.  One size serves both
+// cache types.
+size_t owner_bytes(const tq_pages &p) { return (size_t)tq_align_up((int64_t)p.batch * p.n_kv_heads * sizeof(int2), 256); }
+template <int D>
+int most_workers(int device) {
+  return tq_device_sms(device) * std::max(Shape<float, D>::kOcc * Shape<float, D>::kWarps, Shape<__nv_bfloat16, D>::kOcc * Shape<__nv_bfloat16, D>::kWarps);
+}
+int most_workers(int device, int d) {
+  return d <= 64 ? most_workers<64>(device) : d <= 128 ? most_workers<128>(device) : most_workers<256>(device);
 }
 
-size_t owner_bytes(int grid) { return (size_t)tq_align_up((int64_t)grid * kWarps * sizeof(int4), 256); }
-
 template <typename T, int D, bool WIDE, int PARTS, typename O>
-cudaError_t launch(const PagedArgs &a, int grid, cudaStream_t st) {
+cudaError_t launch(const PagedArgs &a, int device, cudaStream_t st) {
   using S = Shape<T, D>;
   auto kern = attend_paged_kernel<T, D, WIDE, PARTS, O>;
   cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
+  // as many blocks as fit on the GPU at once, fewer where the rows could not give each warp a step
+  const int64_t rows = (int64_t)a.batch * a.heads;
+  const int64_t steps = rows * (a.max_len <= S::kTok ? 1 : (a.max_len - 1) / S::kTok + 1);
+  const int grid = (int)std::min((steps + S::kWarps - 1) / S::kWarps, (int64_t)S::kOcc * tq_device_sms(device));
   tq_prof_begin(TQK_ATTEND_PAGED, st);
-  e = tq_launch_dependent(kern, dim3((unsigned)grid), kThreads, S::kSmem, st, a);
+  e = tq_launch_dependent(kern, dim3((unsigned)grid), S::kThreads, S::kSmem, st, a);
   tq_prof_end(TQK_ATTEND_PAGED, st);
   if (e != cudaSuccess) return e;
+  // the vectors of a row cut into ranges while all blocks fit on the GPU at once
+  const int vecs = a.group * a.d / 4, room = 8 * tq_device_sms(device);
+  const int cuts = (int)std::max((int64_t)1, std::min((int64_t)room / rows, (int64_t)(vecs + 15) / 16));
+  const int each = std::min(kMergeThreads, (vecs + cuts - 1) / cuts);
+  const dim3 mgrid((unsigned)std::min(rows, (int64_t)room), (unsigned)((vecs + each - 1) / each));
   tq_prof_begin(TQK_ATTEND_PAGED_MERGE, st);
-  e = tq_launch_dependent(attend_paged_merge_kernel<O>, dim3((unsigned)grid), kMergeThreads, 0, st, a);
+  e = tq_launch_dependent(attend_paged_merge_kernel<O>, mgrid, kMergeThreads, 0, st, a, (int)S::kWarps, each);
   tq_prof_end(TQK_ATTEND_PAGED_MERGE, st);
   return e;
 }
 
 template <typename T, int PARTS, typename O>
-cudaError_t launch_d(const PagedArgs &a, int grid, cudaStream_t st) {
+cudaError_t launch_d(const PagedArgs &a, int device, cudaStream_t st) {
   const bool wide = a.group > 8;
-  if (a.d <= 64) return wide ? launch<T, 64, true, PARTS, O>(a, grid, st) : launch<T, 64, false, PARTS, O>(a, grid, st);
-  if (a.d <= 128) return wide ? launch<T, 128, true, PARTS, O>(a, grid, st) : launch<T, 128, false, PARTS, O>(a, grid, st);
-  return wide ? launch<T, 256, true, PARTS, O>(a, grid, st) : launch<T, 256, false, PARTS, O>(a, grid, st);
+  if (a.d <= 64) return wide ? launch<T, 64, true, PARTS, O>(a, device, st) : launch<T, 64, false, PARTS, O>(a, device, st);
+  if (a.d <= 128) return wide ? launch<T, 128, true, PARTS, O>(a, device, st) : launch<T, 128, false, PARTS, O>(a, device, st);
+  return wide ? launch<T, 256, true, PARTS, O>(a, device, st) : launch<T, 256, false, PARTS, O>(a, device, st);
 }
 
 }  // namespace
@@ -600,8 +599,7 @@ extern "C" tq_status tq_attend_paged_workspace_size(const tq_pages *pages, int32
   tq_status st = check_attend(pages, max_seq_len, n_q_heads, d);
   if (st != TQ_OK) return st;
   if (!bytes) return tq_fail(TQ_EINVAL, "bytes is NULL");
-  const int grid = attend_grid(*pages, max_seq_len, d);
-  *bytes = owner_bytes(grid) + sizeof(float) * 2 * (size_t)grid * kWarps * piece_floats(n_q_heads / pages->n_kv_heads, d);
+  *bytes = owner_bytes(*pages) + sizeof(float) * 2 * (size_t)most_workers(pages->device, d) * piece_floats(n_q_heads / pages->n_kv_heads, d);
   return TQ_OK;
 }
 
@@ -631,11 +629,10 @@ extern "C" tq_status tq_attend_paged(const tq_pages *pages, const int32_t *seq_l
   PagedArgs a{pages->batch, pages->n_kv_heads, n_q_heads / pages->n_kv_heads, pages->block_size, pages->max_blocks,
               max_seq_len, d, pages->n_blocks, scale != 0.f ? scale : 1.f / sqrtf((float)d), pages->block_table, seq_lens,
               q, k_cache, v_cache, out, FastDiv(pages->block_size), nullptr, nullptr};
-  const int grid = attend_grid(*pages, max_seq_len, d);
-  a.owner = static_cast<int4 *>(ws);
-  a.piece = reinterpret_cast<float *>(static_cast<char *>(ws) + owner_bytes(grid));
-  cudaError_t e = dtype == TQ_F32       ? launch_d<float, 2, float>(a, grid, s)
-                  : out_dtype == TQ_F32 ? launch_d<__nv_bfloat16, 3, float>(a, grid, s)
-                                        : launch_d<__nv_bfloat16, 2, __nv_bfloat16>(a, grid, s);
+  a.owner = static_cast<int2 *>(ws);
+  a.piece = reinterpret_cast<float *>(static_cast<char *>(ws) + owner_bytes(*pages));
+  cudaError_t e = dtype == TQ_F32       ? launch_d<float, 2, float>(a, pages->device, s)
+                  : out_dtype == TQ_F32 ? launch_d<__nv_bfloat16, 3, float>(a, pages->device, s)
+                                        : launch_d<__nv_bfloat16, 2, __nv_bfloat16>(a, pages->device, s);
   return tq_cuda_check(e, "paged attention launch");
 }

@@ -182,9 +182,10 @@ struct Scorer<float, D, WIDE> {
 // Bound: 2 d values per block, read once for the whole group: HBM.  The loads and the division of the work
 // are those of the paged attention, a step being kTok blocks; every warp works alone.
 template <typename T, int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kernel(BlockScoreArgs a) {
+__global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) block_scores_kernel(BlockScoreArgs a) {
   using S = Shape<T, D>;
   using Sc = Scorer<T, D, WIDE>;
+  constexpr int kWarps = S::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Place place[kWarps];
   __shared__ uint32_t masks[kWarps][S::kStages];
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D>::kOcc) block_scores_kern
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-  StepScan scan;
+  StepScan<kWarps> scan;
   scan.run(a.lens, a.batch, a.heads, a.max_len, a.step_tokens);
   const int64_t workers = min((int64_t)gridDim.x * kWarps, scan.total);
   const Deal deal(scan.total + (int64_t)a.batch * a.heads * kRowCost, workers);
@@ -286,10 +287,10 @@ cudaError_t launch_scores_d(BlockScoreArgs a, int device, cudaStream_t st) {
   auto kern = a.group > 8 ? block_scores_kernel<T, D, true> : block_scores_kernel<T, D, false>;
   cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t want = ((int64_t)a.batch * a.heads * ((a.max_blocks - 1) / S::kTok + 1) + kWarps - 1) / kWarps;
+  const int64_t want = ((int64_t)a.batch * a.heads * ((a.max_blocks - 1) / S::kTok + 1) + S::kWarps - 1) / S::kWarps;
   const int64_t most = (int64_t)S::kOcc * tq_device_sms(device);
   tq_prof_begin(TQK_BLOCK_SCORES, st);
-  e = tq_launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), kThreads, S::kSmem, st, a);
+  e = tq_launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), S::kThreads, S::kSmem, st, a);
   tq_prof_end(TQK_BLOCK_SCORES, st);
   return e;
 }

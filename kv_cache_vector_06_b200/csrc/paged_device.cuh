@@ -4,17 +4,16 @@
 
 #include "device_common.cuh"
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-
 // Rows of d padded to D channels; T the cache's type.  A step's keys and values take 64 D bytes of ring.
 template <typename T, int D>
 struct Shape {
   static constexpr int kTok = 32 / sizeof(T);             // tokens per step: 16 (bf16) or 8 (fp32)
   static constexpr int kRow = D * (int)sizeof(T);         // bytes of a padded row
   static constexpr int kCh = kRow / 16;                   // 16-byte chunks of a row
-  static constexpr int kStages = D == 64 ? 4 : 3;
-  static constexpr int kOcc = D == 64 ? 3 : D == 128 ? 2 : 1;  // blocks per SM
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kWarps = D == 256 ? 6 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kOcc = D == 64 ? (sizeof(T) == 2 ? 3 : 2) : D == 128 ? 2 : 1;  // blocks per SM
   static constexpr int kStage = 2 * kTok * kRow;
   static constexpr int kRing = kStages * kStage;          // per warp
   static constexpr int kSmem = kWarps * kRing;
@@ -185,7 +184,8 @@ struct Deal {
 };
 
 // The steps of all (sequence, KV head) rows laid end to end, sequence by sequence: each thread of the
-// block sums a run of sequences, then a block scan.  kThreads threads; has one block barrier.
+// block sums a run of sequences, then a block scan.  Has one block barrier.
+template <int WARPS>
 struct StepScan {
   int b0, b1;           // this thread's sequences
   int len0;             // the first one's length
@@ -193,9 +193,9 @@ struct StepScan {
   int64_t total;
   int heads;
   __device__ __forceinline__ void run(const int32_t *lens, int batch, int n_heads, int max_len, int tok) {
-    __shared__ int64_t wsum[kWarps];
+    __shared__ int64_t wsum[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (batch + kThreads - 1) / kThreads;
+    const int per = (batch + 32 * WARPS - 1) / (32 * WARPS);
     heads = n_heads;
     b0 = (int)min((int64_t)threadIdx.x * per, (int64_t)batch);
     b1 = (int)min((int64_t)b0 + per, (int64_t)batch);
@@ -214,7 +214,7 @@ struct StepScan {
     total = 0;
     before = incl - mine;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const int64_t x = wsum[w];
       if (w < warp) before += x;
       total += x;
@@ -230,7 +230,8 @@ struct Place {
 
 // With `extra` units of work counted in front of every row's steps (what a row costs beside them): the
 // thread that holds unit `pos` of all rows writes where it lies.
-__device__ __forceinline__ void find_unit(const StepScan &s, int64_t pos, int extra, const int32_t *lens, int max_len, int tok, Place &out) {
+template <int WARPS>
+__device__ __forceinline__ void find_unit(const StepScan<WARPS> &s, int64_t pos, int extra, const int32_t *lens, int max_len, int tok, Place &out) {
   const int64_t front = s.before + (int64_t)s.b0 * s.heads * extra;
   int64_t left = pos - front;
   if (left < 0 || left >= s.mine + (int64_t)(s.b1 - s.b0) * s.heads * extra) return;

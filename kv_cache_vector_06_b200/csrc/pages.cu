@@ -1,6 +1,7 @@
 // Paged-cache bookkeeping: block tables, lengths and slot maps from request lengths
 // (tq_page_extend), and the append of uncompressed rows with the channel bounds of every block's
 // keys (tq_append_kv).
+#include <algorithm>
 #include <atomic>
 
 #include "paged_device.cuh"
@@ -238,7 +239,7 @@ constexpr int64_t kExtendOneBlock = 2048;
 constexpr int kExtendBlocksPerSm = 4;
 
 struct AppendArgs {
-  int batch, heads, bs, max_blocks, d;
+  int batch, heads, bs, max_blocks, d, per_warp;
   int64_t n_blocks, n_rows, ld, units;
   const int32_t *table, *lens, *granted;
   const int64_t *offsets;
@@ -276,10 +277,12 @@ __device__ __forceinline__ uint4 shfl4(const uint4 &v, int src) {
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) { return __ldcs(p); }
 
 constexpr int kAppendWarps = 8, kAppendAhead = 4;
+constexpr int64_t kAppendBytes = 16384;
 
 // A copy with a reduction riding along: bound by HBM (4 rows of d in and out per (token, head), and two per
-// block).  A warp takes one KV head of one touched block, whose rows lie together in the cache; the
-// block's warps take neighbouring heads, whose rows lie together in the input.  Lanes hold 16-byte chunks,
+// block).  A warp takes one KV head of one touched block, whose rows lie together in the cache, or per_warp
+// heads where these rows are short (finding the block costs as much as 8 KB of copy); the block's warps take
+// neighbouring heads, whose rows lie together in the input.  Lanes hold 16-byte chunks,
 // 32 / chunks rows at a time, kAppendAhead loads of each array in flight.
 //
 // Work unit u of sequence b: u - (offsets[b] / bs + 2 b) is the touched block's number; a sequence of n
@@ -290,8 +293,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t w = blockIdx.x * (int64_t)kAppendWarps + (threadIdx.x >> 5);
-  const int64_t u = w / a.heads;
-  const int h = (int)(w - u * a.heads);
+  const int parts = (a.heads + a.per_warp - 1) / a.per_warp;
+  const int64_t u = w / parts;
+  const int h0 = (int)(w - u * parts) * a.per_warp, h1 = min(h0 + a.per_warp, a.heads);
   if (u >= a.units) return;
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
@@ -311,67 +315,69 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   const int64_t begin = j * a.bs;  // the block's first token
   const int t0 = begin > before ? 0 : (int)(before - begin);
   const int t1 = begin + a.bs < len ? a.bs : (int)(len - begin);
-  const int64_t blk = (int64_t)e * a.heads + h;
   const int chunks = a.d * (int)sizeof(T) / 16;
   const int64_t ld = a.ld * (int64_t)sizeof(T) / 16;
-  const uint4 *k = reinterpret_cast<const uint4 *>(a.k) + (row0 - before + begin) * ld + (int64_t)h * chunks;
-  const uint4 *v = reinterpret_cast<const uint4 *>(a.v) + (row0 - before + begin) * ld + (int64_t)h * chunks;
-  uint4 *kc = reinterpret_cast<uint4 *>(a.kc) + blk * a.bs * chunks, *vc = reinterpret_cast<uint4 *>(a.vc) + blk * a.bs * chunks;
-  uint4 *bound = reinterpret_cast<uint4 *>(a.bounds) + blk * 2 * chunks;
   const int at_once = chunks < 32 ? 32 / chunks : 1;  // rows per pass
   const int sub = chunks < 32 ? lane / chunks : 0;
-  for (int c0 = 0; c0 < chunks; c0 += 32) {
-    const int c = chunks < 32 ? lane - sub * chunks : c0 + lane;
-    const bool on = c < chunks && sub < at_once;
-    uint4 mn, mx;
-    bool any = false;
-    for (int t = t0 + sub; on && t < t1; t += kAppendAhead * at_once) {
-      uint4 x[kAppendAhead], y[kAppendAhead];
+  for (int h = h0; h < h1; ++h) {
+    const int64_t blk = (int64_t)e * a.heads + h;
+    const uint4 *k = reinterpret_cast<const uint4 *>(a.k) + (row0 - before + begin) * ld + (int64_t)h * chunks;
+    const uint4 *v = reinterpret_cast<const uint4 *>(a.v) + (row0 - before + begin) * ld + (int64_t)h * chunks;
+    uint4 *kc = reinterpret_cast<uint4 *>(a.kc) + blk * a.bs * chunks, *vc = reinterpret_cast<uint4 *>(a.vc) + blk * a.bs * chunks;
+    uint4 *bound = reinterpret_cast<uint4 *>(a.bounds) + blk * 2 * chunks;
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const int c = chunks < 32 ? lane - sub * chunks : c0 + lane;
+      const bool on = c < chunks && sub < at_once;
+      uint4 mn, mx;
+      bool any = false;
+      for (int t = t0 + sub; on && t < t1; t += kAppendAhead * at_once) {
+        uint4 x[kAppendAhead], y[kAppendAhead];
 #pragma unroll
-      for (int i = 0; i < kAppendAhead; ++i) {
-        const int tt = t + i * at_once;
-        if (tt < t1) {
-          x[i] = ld_stream(k + tt * ld + c);
-          if (a.kc) y[i] = ld_stream(v + tt * ld + c);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAppendAhead; ++i) {
-        const int tt = t + i * at_once;
-        if (tt < t1) {
-          if (a.kc) {
-            kc[(int64_t)tt * chunks + c] = x[i];
-            vc[(int64_t)tt * chunks + c] = y[i];
+        for (int i = 0; i < kAppendAhead; ++i) {
+          const int tt = t + i * at_once;
+          if (tt < t1) {
+            x[i] = ld_stream(k + tt * ld + c);
+            if (a.kc) y[i] = ld_stream(v + tt * ld + c);
           }
-          if (!any) mn = mx = x[i];
-          any = true;
-          widen<T>(mn, mx, x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAppendAhead; ++i) {
+          const int tt = t + i * at_once;
+          if (tt < t1) {
+            if (a.kc) {
+              kc[(int64_t)tt * chunks + c] = x[i];
+              vc[(int64_t)tt * chunks + c] = y[i];
+            }
+            if (!any) mn = mx = x[i];
+            any = true;
+            widen<T>(mn, mx, x[i]);
+          }
         }
       }
-    }
-    if (!a.bounds) continue;
-    // the rows of one pass lie `chunks` lanes apart; at most t1 - t0 of them hold anything
-    const int parts = min(at_once, t1 - t0);
-    for (int i = 1; i < parts; ++i) {
-      const int src = (c + i * chunks) & 31;
-      const uint4 l = shfl4(mn, src), m = shfl4(mx, src);
-      uint4 unused = mx;
-      if (sub == 0 && on) {
-        widen<T>(mn, unused, l);
-        unused = mn;
-        widen<T>(unused, mx, m);
-      }
-    }
-    if (sub == 0 && on) {
-      if (t0 > 0) {  // begun before: its bounds are widened
-        const uint4 l = bound[c], m = bound[chunks + c];
+      if (!a.bounds) continue;
+      // the rows of one pass lie `chunks` lanes apart; at most t1 - t0 of them hold anything
+      const int parts = min(at_once, t1 - t0);
+      for (int i = 1; i < parts; ++i) {
+        const int src = (c + i * chunks) & 31;
+        const uint4 l = shfl4(mn, src), m = shfl4(mx, src);
         uint4 unused = mx;
-        widen<T>(mn, unused, l);
-        unused = mn;
-        widen<T>(unused, mx, m);
+        if (sub == 0 && on) {
+          widen<T>(mn, unused, l);
+          unused = mn;
+          widen<T>(unused, mx, m);
+        }
       }
-      bound[c] = mn;
-      bound[chunks + c] = mx;
+      if (sub == 0 && on) {
+        if (t0 > 0) {  // begun before: its bounds are widened
+          const uint4 l = bound[c], m = bound[chunks + c];
+          uint4 unused = mx;
+          widen<T>(mn, unused, l);
+          unused = mn;
+          widen<T>(unused, mx, m);
+        }
+        bound[c] = mn;
+        bound[chunks + c] = mx;
+      }
     }
   }
 }
@@ -464,9 +470,12 @@ extern "C" tq_status tq_append_kv(const tq_pages *pages, const int32_t *seq_lens
   st = dev_scope.enter(pages->device);
   if (st != TQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  AppendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, d, pages->n_blocks, n_rows, ld,
+  const int64_t held = (int64_t)pages->block_size * d * esz * (k_cache ? 4 : 2);  // bytes in and out per (block, head)
+  const int per_warp = (int)std::max((int64_t)1, std::min((int64_t)pages->n_kv_heads, kAppendBytes / held));
+  AppendArgs a{pages->batch, pages->n_kv_heads, pages->block_size, pages->max_blocks, d, per_warp, pages->n_blocks, n_rows, ld,
                units, pages->block_table, seq_lens, granted, row_offsets, k_new, v_new, k_cache, v_cache, bounds};
-  const unsigned grid = (unsigned)((units * pages->n_kv_heads + kAppendWarps - 1) / kAppendWarps);
+  const int parts = (pages->n_kv_heads + per_warp - 1) / per_warp;
+  const unsigned grid = (unsigned)((units * parts + kAppendWarps - 1) / kAppendWarps);
   tq_prof_begin(TQK_APPEND_KV, s);
   const cudaError_t e = tq_launch_dependent(dtype == TQ_F32 ? append_kv_kernel<float> : append_kv_kernel<__nv_bfloat16>, dim3(grid),
                                             32 * kAppendWarps, 0, s, a);

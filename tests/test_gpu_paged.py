@@ -354,6 +354,35 @@ def test_attend_workspace_reused(tq):
         check_attend(tq, lens, 2, 4, 16, 128, BF16, seed=20 + seed, ws=ws)
 
 
+def test_attend_captured_calls_share_a_workspace(tq):
+    """Two captured calls of different shapes and an eager one on one workspace, replayed in turn: the same bits
+    every time, whatever the call before left there."""
+    d, block, group = 128, 16, 4
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8).cuda()
+    calls = []
+    for lens, n_kv in (([3000, 20, 700], 2), ([9000], 1), ([5, 4000, 0, 33] * 40, 4)):
+        table, n_blocks = tables(lens, max(-(-n // block) for n in lens), block, seed=n_kv)
+        kc, vc = (rows(n_blocks, n_kv, block, d, seed=s, dtype=BF16).cuda() for s in (1, 2))
+        q, out = rows(len(lens), n_kv * group, d, seed=3, dtype=BF16).cuda(), torch.empty(len(lens), n_kv * group, d).cuda()
+        pages, n = tq.Pages(i32(table), n_kv, block, n_blocks), i32(lens)
+        calls.append((lambda p=pages, n=n, m=table.shape[1] * block, q=q, k=kc, v=vc, o=out:
+                      tq.attend_paged(p, n, m, q, k, v, out=o, ws=ws), out))
+    want = []
+    for call, out in calls:
+        ws.random_(256)
+        want.append(call().clone())
+    graphs = []
+    for call, out in calls[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g.replay)
+    for i in (0, 1, 1, 0, 2, 0, 0, 2, 1, 2, 0):
+        calls[i][1].fill_(math.nan)
+        (graphs + [calls[2][0]])[i]()
+        assert torch.equal(calls[i][1], want[i]), i
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_far_offsets(tq, dtype):
     """A cache whose element offsets pass 2^32: append to its last blocks, then score and attend there."""
