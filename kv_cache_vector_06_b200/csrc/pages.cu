@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   const int b = lo;
   const int64_t row0 = a.offsets[b];
   const int add = a.granted[b], len = a.lens[b];
-  if (add <= 0 || len < add || len > (int64_t)a.max_blocks * a.bs || row0 + add > a.n_rows) return;
+  if (add <= 0 || len < add || len > (int64_t)a.max_blocks * a.bs || row0 < 0 || row0 + add > a.n_rows) return;
   const int before = len - add;
   const int64_t j = before / a.bs + (u - (row0 / a.bs + 2 * (int64_t)b));
   if (j > (len - 1) / a.bs) return;

@@ -472,6 +472,14 @@ def _raw_stream(device: int, stream) -> int:
     return _current_stream(device) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor that a call makes for itself: kept from reuse while the call's own stream still works on it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 class Pages:
     """Paged-cache addressing (tq_pages): the block table [batch, max_blocks] and the cache's shape.
     Holds the table's tensor; the calls below run on its device."""
@@ -519,15 +527,15 @@ def page_extend(pages: Pages, seq_lens, new_lens, free_blocks, free_head, n_rows
     if new_slots is None:
         if n_rows is None:
             raise ValueError("n_rows or new_slots is required")
-        new_slots = torch.empty(n_rows * pages.n_kv_heads, dtype=i64, device=free_head.device)
+        new_slots = _new(n_rows * pages.n_kv_heads, i64, free_head.device, stream)
     if seq_lens_out is None:
-        seq_lens_out = torch.empty(n, dtype=i32, device=free_head.device)
+        seq_lens_out = _new(n, i32, free_head.device, stream)
     if granted is None:
-        granted = torch.empty(n, dtype=i32, device=free_head.device)
+        granted = _new(n, i32, free_head.device, stream)
     if free_head_out is None:
-        free_head_out = torch.empty(1, dtype=i32, device=free_head.device)
+        free_head_out = _new(1, i32, free_head.device, stream)
     if row_offsets is None:
-        row_offsets = torch.empty(n + 1, dtype=i64, device=free_head.device)
+        row_offsets = _new(n + 1, i64, free_head.device, stream)
     n_free, n_slots, arg = free_blocks.numel(), new_slots.numel(), pages._arg
     _check(LIB.tq_page_extend(
         pages.ref, arg(seq_lens, "seq_lens", i32, n), arg(new_lens, "new_lens", i32, n),
@@ -575,7 +583,7 @@ def block_scores(pages: Pages, seq_lens, q, bounds, out=None, stream=None):
     ([batch, n_q_heads, d]) with the keys of every block, from the bounds that append_kv keeps."""
     qp, hq, d = _queries(pages, q)
     if out is None:
-        out = torch.empty(pages.rows, pages.max_blocks, dtype=torch.float32, device=q.device)
+        out = _new((pages.rows, pages.max_blocks), torch.float32, q.device, stream)
     _check(LIB.tq_block_scores(
         pages.ref, pages._arg(seq_lens, "seq_lens", torch.int32, pages.batch), qp, _dtype_code(q), hq, d,
         pages._cache(bounds, "bounds", 2, d, q.dtype),
@@ -590,9 +598,9 @@ def select_blocks(pages: Pages, seq_lens, scores, n_keep: int, n_first: int = 1,
     pages.selected(table) reads the same cache through it; for make_attn_desc it is the block_table of
     batch * n_kv_heads sequences with n_kv_heads = 1."""
     if table is None:
-        table = torch.empty(pages.rows, max(n_keep, 0), dtype=torch.int32, device=scores.device)
+        table = _new((pages.rows, max(n_keep, 0)), torch.int32, scores.device, stream)
     if lens is None:
-        lens = torch.empty(pages.rows, dtype=torch.int32, device=scores.device)
+        lens = _new(pages.rows, torch.int32, scores.device, stream)
     arg, i32 = pages._arg, torch.int32
     _check(LIB.tq_select_blocks(
         pages.ref, arg(seq_lens, "seq_lens", i32, pages.batch),
@@ -616,9 +624,9 @@ def attend_paged(pages: Pages, seq_lens, max_seq_len: int, q, k_cache, v_cache, 
     qp, hq, d = _queries(pages, q)
     dev, dt = pages.device, q.dtype
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _new(q.shape, torch.float32, q.device, stream)
     if ws is None:
-        ws = torch.empty(attend_paged_workspace_size(pages, max_seq_len, hq, d), dtype=torch.uint8, device=q.device)
+        ws = _new(attend_paged_workspace_size(pages, max_seq_len, hq, d), torch.uint8, q.device, stream)
     _check(LIB.tq_attend_paged(
         pages.ref, pages._arg(seq_lens, "seq_lens", torch.int32, pages.batch), max_seq_len, qp,
         pages._cache(k_cache, "k_cache", pages.block_size, d, dt), pages._cache(v_cache, "v_cache", pages.block_size, d, dt),

@@ -104,6 +104,27 @@ def test_extend_odd_values(tq):
     assert slots.tolist() == [-1] * 6 and head.item() == 1 and off.tolist() == [0]
 
 
+def test_extend_many_heads(tq):
+    """More heads than a block has threads, whole prompts and single tokens."""
+    for n_kv in (1100, 514):
+        table, used = tables([5, 0, 16], 9, 16, seed=1)
+        check_extend(tq, table, [5, 0, 16], [100, 7, 1], np.arange(used, used + 12), 1, 120, n_kv, 16, used + 12, False)
+
+
+def test_extend_is_stable_under_shifted_slots(tq):
+    """new_slots at any 8-byte address (the wide stores want 16 or 32)."""
+    for n_kv in (8, 2, 3):
+        buf = torch.full((600 * n_kv + 8,), 77, dtype=torch.int64).cuda()
+        for shift in (0, 1, 2, 4):
+            table, used = tables([30, 0], 40, 16, seed=2)
+            pages, free = tq.Pages(i32(table), n_kv, 16, used + 60), np.arange(used, used + 50)
+            slots = buf[shift:shift + 600 * n_kv]
+            tq.page_extend(pages, i32([30, 0]), i32([1, 555]), i32(free), i32([0]), new_slots=slots)
+            ref = paged.extend(table, [30, 0], [1, 555], free, 0, 600, n_kv, 16, used + 60)
+            assert np.array_equal(slots.cpu().numpy(), ref[5]) and buf[600 * n_kv + shift:].eq(77).all()
+            buf.fill_(77)
+
+
 # ------------------------------------------------------------------------------------ append_kv
 def append_case(tq, lens, granted, n_kv, block, d, dtype, seed, gap=0, offsets=None, table=None, caches=True, with_bounds=True,
                 n_rows=None):
@@ -347,6 +368,11 @@ def test_attend_odd_tables(tq, dtype):
     check_attend(tq, [1000, -5, 33, 30], 2, 4, 16, 64, dtype, seed=14, table=t, max_len=33)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_no_tokens_at_all(tq, dtype):
+    check_attend(tq, [5, 0, 9], 2, 4, 16, 64, dtype, seed=15, max_len=0)
+
+
 def test_attend_workspace_reused(tq):
     """One workspace, filled with NaN, for calls of different shapes in a row."""
     ws = torch.full((1 << 24,), 255, dtype=torch.uint8).cuda()
@@ -506,6 +532,31 @@ def test_serving_steps_on_two_streams(tq):
     for x, y in zip(alone, both):
         for u, w in zip(x, y):
             assert all(torch.equal(a, b) for a, b in zip(u, w))
+
+
+def test_calls_on_a_given_stream(tq):
+    """stream=: the work runs there, not on the current stream, and what the calls allocate stays theirs."""
+    n_kv, group, d, block = 2, 4, 128, 16
+    table, n_blocks = tables([700], 44, block, 3)
+    pages, lens = tq.Pages(i32(table), n_kv, block, n_blocks), i32([700])
+    k, v = (rows(700, n_kv, d, seed=s, dtype=BF16).cuda() for s in (1, 2))
+    q = rows(1, n_kv * group, d, seed=3, dtype=BF16).cuda()
+    kc, vc = (torch.zeros(n_blocks, n_kv, block, d, dtype=BF16).cuda() for _ in (0, 1))
+    bd, off = torch.zeros(n_blocks, n_kv, 2, d, dtype=BF16).cuda(), torch.tensor([0, 700]).cuda()
+
+    def run(stream):
+        for x in (kc, vc, bd):
+            x.zero_()
+        torch.cuda.synchronize()
+        tq.append_kv(pages, lens, lens, off, k, v, kc, vc, bd, stream=stream)
+        t, n = tq.select_blocks(pages, lens, tq.block_scores(pages, lens, q, bd, stream=stream), 7, stream=stream)
+        o = tq.attend_paged(pages.selected(t), n, 7 * block, q.view(n_kv, group, d), kc, vc, stream=stream)
+        torch.empty(1 << 22, device="cuda").fill_(math.nan)  # takes what the current stream may reuse
+        torch.cuda.synchronize()
+        return t, n, o
+
+    for x, y in zip(run(None), run(torch.cuda.Stream())):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("vlayout", [0, 1])
