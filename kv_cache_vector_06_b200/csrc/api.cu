@@ -94,6 +94,8 @@ tq_status tq_fail(tq_status st, const char *fmt, ...) {
   return st;
 }
 
+void tq_clear_error() { g_err[0] = 0; }
+
 tq_status tq_cuda_check(cudaError_t e, const char *what) {
   if (e == cudaSuccess) return TQ_OK;
   return tq_fail(TQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));

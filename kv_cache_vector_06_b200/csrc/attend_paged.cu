@@ -54,8 +54,14 @@ struct Stream {
   static constexpr bool kBf = sizeof(T) == 2;
   static constexpr int kKg = S::kCh / 4;                        // 64-byte groups of a row
   static constexpr int kQRegs = kKg * (WIDE ? 8 : 4) * (kBf ? 1 : 2);
-  static constexpr bool kQInRegs = kQRegs <= 64;
+  static constexpr bool kQInRegs = kQRegs <= (kBf ? 32 : 64);
   static constexpr int kQ = kQInRegs ? kKg : 1;
+  // Queries that the registers do not hold lie in shared memory, once for the block's warps, in the order in
+  // which the lanes take them; where a warp works alone, or where they would cost the second block of the SM,
+  // each step asks the first-level cache for them (32 x 8 heads of 256 channels, fp32: 138 us, from the cache 172).
+  static constexpr int kQBytes = kKg * (WIDE ? 2 : 1) * (kBf ? 1 : 2) * 512;
+  static constexpr bool kQInSmem = !kQInRegs && kQBytes <= 16384;
+  static constexpr int kSmem = S::kSmem + (kQInSmem ? kQBytes : 0);
   static constexpr int kNt = D / 8;
   static constexpr int kH = WIDE ? 2 : 1;                       // heads per lane: lane / 4 and 8 + lane / 4
 
@@ -74,9 +80,26 @@ struct Stream {
     }
   }
 
-  // One step: keys at kbase, values at vbase, tokens `valid`.
-  __device__ __forceinline__ void step(const PagedArgs &a, int64_t row, unsigned kbase, unsigned vbase, uint32_t valid, float sc,
-                                       int lane) {
+  // This lane's part of group kg in shared memory: parts of 512 bytes.
+  static __device__ __forceinline__ unsigned q_at(unsigned qs, int kg, int lane) {
+    return qs + (unsigned)(kg * kH * (kBf ? 1 : 2) * 512 + lane * 16);
+  }
+  static __device__ __forceinline__ void put_q(const PagedArgs &a, int64_t row, unsigned qs, int kg, int lane) {
+    uint4 raw[kH];
+    uint32_t f[kH][kBf ? 1 : 2][4];
+    load_q<T, kH>(raw, a.q, row, a.group, a.d, kg, lane);
+    make_q<T, kH>(f, raw);
+#pragma unroll
+    for (int x = 0; x < kH * (kBf ? 1 : 2); ++x) {
+      const auto &v = f[x / (kBf ? 1 : 2)][x % (kBf ? 1 : 2)];
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(q_at(qs, kg, lane) + 512 * x), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                   : "memory");
+    }
+  }
+
+  // One step: keys at kbase, values at vbase, tokens `valid`; queries at qs where they are in shared memory.
+  __device__ __forceinline__ void step(const PagedArgs &a, int64_t row, unsigned qs, unsigned kbase, unsigned vbase, uint32_t valid,
+                                       float sc, int lane) {
     constexpr int kT = S::kTok / 8;
     const int c = lane & 3, r = lane >> 2;
     // chunk 4 kg + c of token r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
@@ -89,9 +112,14 @@ struct Stream {
 #pragma unroll
     for (int kg = 0; kg < kKg; ++kg) {
       if constexpr (!kQInRegs) {
-        uint4 raw[kH];
-        load_q<T, kH>(raw, a.q, row, a.group, a.d, kg, lane);
-        make_q<T, kH>(qf[0], raw);
+        if (kQInSmem && qs != 0) {
+#pragma unroll
+          for (int x = 0; x < kH * (kBf ? 1 : 2); ++x) lds128(qf[0][x / (kBf ? 1 : 2)][x % (kBf ? 1 : 2)], q_at(qs, kg, lane) + 512 * x);
+        } else {
+          uint4 raw[kH];
+          load_q<T, kH>(raw, a.q, row, a.group, a.d, kg, lane);
+          make_q<T, kH>(qf[0], raw);
+        }
       }
       const auto &f = qf[kQInRegs ? kg : 0];
 #pragma unroll
@@ -369,6 +397,11 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
 #pragma unroll
       for (int kg = 0; kg < St::kKg; ++kg) make_q<T, St::kH>(st.qf[kg], raw[kg]);
     }
+    const unsigned qs = St::kQInSmem && !solo ? smem_addr(smem) + S::kSmem : 0;
+    if (St::kQInSmem && !solo) {
+      for (int kg = warp; kg < St::kKg; kg += kWarps) St::put_q(a, row, qs, kg, lane);
+      __syncthreads();
+    }
     st.clear();
     for (int i = 0; i < n; ++i) {
       cp_wait<S::kStages - 2>();
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
       next = entry(i + S::kStages);
       const int stage = i % S::kStages;
       const unsigned kb = ring + stage * S::kStage;
-      st.step(a, row, kb, kb + S::kTok * S::kRow, masks[warp][stage], sc, lane);
+      st.step(a, row, qs, kb, kb + S::kTok * S::kRow, masks[warp][stage], sc, lane);
     }
     cp_wait<0>();
     __syncwarp();
@@ -562,15 +595,16 @@ int most_workers(int device, int d) {
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 cudaError_t launch(const PagedArgs &a, int device, cudaStream_t st) {
   using S = Shape<T, D>;
+  constexpr int kSmem = Stream<T, D, WIDE, PARTS>::kSmem;
   auto kern = attend_paged_kernel<T, D, WIDE, PARTS, O>;
-  cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), S::kSmem);
+  cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), kSmem);
   if (e != cudaSuccess) return e;
   // as many blocks as fit on the GPU at once, fewer where the rows could not give each warp a step
   const int64_t rows = (int64_t)a.batch * a.heads;
   const int64_t steps = rows * (a.max_len <= S::kTok ? 1 : (a.max_len - 1) / S::kTok + 1);
   const int grid = (int)std::min((steps + S::kWarps - 1) / S::kWarps, (int64_t)S::kOcc * tq_device_sms(device));
   tq_prof_begin(TQK_ATTEND_PAGED, st);
-  e = tq_launch_dependent(kern, dim3((unsigned)grid), S::kThreads, S::kSmem, st, a);
+  e = tq_launch_dependent(kern, dim3((unsigned)grid), S::kThreads, kSmem, st, a);
   tq_prof_end(TQK_ATTEND_PAGED, st);
   if (e != cudaSuccess) return e;
   // the vectors of a row cut into ranges while all blocks fit on the GPU at once

@@ -20,7 +20,7 @@ int tq_device_sms(int device) {
 }
 
 tq_status tq_check_pages(const tq_pages *p) {
-  tq_fail(TQ_OK, "%s", "");
+  tq_clear_error();
   if (!p) return tq_fail(TQ_EINVAL, "pages is NULL");
   if (p->batch < 0 || p->n_kv_heads <= 0 || p->block_size <= 0 || p->max_blocks <= 0 || p->n_blocks < 0)
     return tq_fail(TQ_EINVAL, "pages: batch=%d n_kv_heads=%d block_size=%d max_blocks=%d n_blocks=%lld", p->batch,

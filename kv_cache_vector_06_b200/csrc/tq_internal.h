@@ -56,6 +56,7 @@ struct tq_ctx {
 // ---------------------------------------------------------------- host helpers (api.cu)
 tq_status tq_fail(tq_status st, const char *fmt, ...);
 tq_status tq_cuda_check(cudaError_t e, const char *what);
+void tq_clear_error();  // empties the thread's tq_last_error()
 // Makes a device current for the duration of one C-ABI call and restores the caller's
 // current device when the call returns (the work itself is only enqueued).
 class DeviceScope {

@@ -627,11 +627,13 @@ def attend_paged(pages: Pages, seq_lens, max_seq_len: int, q, k_cache, v_cache, 
         out = _new(q.shape, torch.float32, q.device, stream)
     if ws is None:
         ws = _new(attend_paged_workspace_size(pages, max_seq_len, hq, d), torch.uint8, q.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        _dev(ws, dev, "ws")
     _check(LIB.tq_attend_paged(
         pages.ref, pages._arg(seq_lens, "seq_lens", torch.int32, pages.batch), max_seq_len, qp,
         pages._cache(k_cache, "k_cache", pages.block_size, d, dt), pages._cache(v_cache, "v_cache", pages.block_size, d, dt),
         _dtype_code(q), hq, d, scale, pages._arg(out, "out", out.dtype, q.shape), _dtype_code(out),
-        _dev(ws, dev, "ws"), ws.numel() * ws.element_size(), _raw_stream(dev, stream)))
+        ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev, stream)))
     return out
 
 
