@@ -351,15 +351,13 @@ __device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = 2047 - kPer * threadIdx.x;
   int cnt[kPer], sum = 0;  // from the thread's largest digit down
 #pragma unroll
-  for (int i = 0; i < kPer; i += 4) {
-    int4 *mine = reinterpret_cast<int4 *>(hist + top - 3 - i);
-    const int4 v = *mine;
-    *mine = make_int4(0, 0, 0, 0);
-    cnt[i] = v.w;
-    cnt[i + 1] = v.z;
-    cnt[i + 2] = v.y;
-    cnt[i + 3] = v.x;
-    sum += v.x + v.y + v.z + v.w;
+  for (int i = 0; i < kPer; i += 2) {
+    int2 *mine = reinterpret_cast<int2 *>(hist + top - 1 - i);
+    const int2 v = *mine;
+    *mine = make_int2(0, 0);
+    cnt[i] = v.y;
+    cnt[i + 1] = v.x;
+    sum += v.x + v.y;
   }
   int s = sum;
 #pragma unroll
@@ -396,9 +394,10 @@ __device__ __forceinline__ void cut_digit(int *hist, int need, int &digit, int &
 // pass in index order writes the blocks above that key and the first ones at it.  Each thread holds PER
 // consecutive keys, so that index order is thread order; rows longer than a block's PER * THREADS keys go
 // through in chunks, read again for each pass, and so do those where a digit's keys outgrow the list.
-// Latency bounds it: a dozen barriers and scans.  Tables of up to 2048 blocks take 256 threads (64 sequences x
-// 8 heads of 64 .. 2048 blocks: 8.7 us per call in a row of calls, 10.8 with 512, 12.2 with 128), longer ones
-// 512.  The next kernel is let in late: its waiting blocks crowd this one's onto fewer SMs (11.1 us).
+// Latency bounds it: a dozen barriers and scans, so a table takes as few threads as hold its keys (64 sequences x
+// 8 heads of 64 .. 2048 blocks: 8.7 us per call in a row of calls with 256 threads, 10.8 with 512, 12.2 with
+// 128; 16 rows of 16383 blocks: 13 us with 1024, 24 with 512 in two chunks).  The next kernel is let in late:
+// its waiting blocks crowd this one's onto fewer SMs (11.1 us).
 template <int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS) select_blocks_kernel(SelectArgs a) {
   constexpr int kChunk = PER * THREADS;
@@ -431,16 +430,27 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(SelectArgs a) {
   }
   const int lo = a.first, hi = n - a.last;  // candidates [lo, hi); the others are always chosen
   uint32_t k[PER];
+  const int off = (int)((reinterpret_cast<uintptr_t>(scores) >> 2) & 3);  // the row's place in its 16 bytes
   auto load = [&](int j0) {  // keys of blocks j0 + PER * thread ..; 0 outside the candidates, below every key
     const int j = j0 + PER * threadIdx.x;
-    if ((a.max_blocks & 3) == 0 && j + PER <= n) {
+    if (j + PER + (off ? 4 : 0) <= n) {
+      // whole 16-byte loads from the row's aligned start on, shifted
+      float f[PER + 4];
 #pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(scores + j + i));
-        k[i] = order_key(v.x);
-        k[i + 1] = order_key(v.y);
-        k[i + 2] = order_key(v.z);
-        k[i + 3] = order_key(v.w);
+      for (int i = 0; i < PER + 4; i += 4) {
+        if (i == PER && off == 0) break;
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(scores - off + j + i));
+        f[i] = v.x;
+        f[i + 1] = v.y;
+        f[i + 2] = v.z;
+        f[i + 3] = v.w;
+      }
+      if (off == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) k[i] = order_key(f[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) k[i] = order_key(off == 1 ? f[i + 1] : off == 2 ? f[i + 2] : f[i + 3]);
       }
       if (j < lo || j + PER > hi) {
 #pragma unroll
@@ -591,8 +601,11 @@ extern "C" tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_
                pages->n_blocks, pages->block_table, seq_lens, scores, sel_table, sel_lens};
   tq_prof_begin(TQK_SELECT_BLOCKS, s);
   const unsigned grid = (unsigned)(pages->batch * pages->n_kv_heads);
-  const cudaError_t e = pages->max_blocks <= 2048 ? tq_launch_dependent(select_blocks_kernel<256, 8>, dim3(grid), 256, 0, s, a)
-                                                  : tq_launch_dependent(select_blocks_kernel<512, 16>, dim3(grid), 512, 0, s, a);
+  const int n = pages->max_blocks;
+  const cudaError_t e = n <= 512    ? tq_launch_dependent(select_blocks_kernel<128, 4>, dim3(grid), 128, 0, s, a)
+                        : n <= 2048 ? tq_launch_dependent(select_blocks_kernel<256, 8>, dim3(grid), 256, 0, s, a)
+                        : n <= 8192 ? tq_launch_dependent(select_blocks_kernel<512, 16>, dim3(grid), 512, 0, s, a)
+                                    : tq_launch_dependent(select_blocks_kernel<1024, 16>, dim3(grid), 1024, 0, s, a);
   tq_prof_end(TQK_SELECT_BLOCKS, s);
   return tq_cuda_check(e, "block selection launch");
 }
