@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
     // block of this lane's token (of the whole step where it lies in one block)
     auto entry = [&](int i) {
       const int t = (first + rank + i * team) * S::kTok + (whole ? 0 : (lane & (S::kTok - 1)));
-      return i < n && t < len ? __ldg(table + a.by_bs(t)) : -1;
+      return i < n && t < len ? table[a.by_bs(t)] : -1;
     };
     auto issue = [&](int i, int e) {
       const int stage = i % S::kStages;

@@ -124,7 +124,7 @@ struct Scorer<float, D, WIDE> {
         const int ch = lane % kLanes + 32 * v;
         q[h][v] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (h0 + h < a.group && 4 * ch < a.d)
-          q[h][v] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + (row * a.group + h0 + h) * a.d) + ch);
+          q[h][v] = *(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + (row * a.group + h0 + h) * a.d) + ch);
       }
   }
   __device__ __forceinline__ void ask(const BlockScoreArgs &a, int64_t row, int lane) {
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) bloc
     const int32_t *table = a.table + (int64_t)b * a.max_blocks;
     auto entry = [&](int i) {
       const int j = (first + i) * S::kTok + (lane & (S::kTok - 1));
-      return i < n && j < held ? __ldg(table + j) : -1;
+      return i < n && j < held ? table[j] : -1;
     };
     auto issue = [&](int i, int e) {
       const int stage = i % S::kStages;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(SelectArgs a) {
 #pragma unroll
       for (int i = 0; i < PER + 4; i += 4) {
         if (i == PER && off == 0) break;
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(scores - off + j + i));
+        const float4 v = *(reinterpret_cast<const float4 *>(scores - off + j + i));
         f[i] = v.x;
         f[i + 1] = v.y;
         f[i + 2] = v.z;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(THREADS) select_blocks_kernel(SelectArgs a) {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) k[i] = j + i >= lo && j + i < hi ? order_key(__ldg(scores + j + i)) : 0;
+      for (int i = 0; i < PER; ++i) k[i] = j + i >= lo && j + i < hi ? order_key(scores[j + i]) : 0;
     }
   };
   const bool once = n <= kChunk;

@@ -109,7 +109,7 @@ __device__ __forceinline__ void load_q(uint4 (&v)[H], const void *q, int64_t row
     const int hd = (lane >> 2) + 8 * x;
     v[x] = make_uint4(0u, 0u, 0u, 0u);
     if (hd < group && ch < d * (int)sizeof(T) / 16)
-      v[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(q) + (row * group + hd) * d) + ch);
+      v[x] = *(reinterpret_cast<const uint4 *>(static_cast<const T *>(q) + (row * group + hd) * d) + ch);
   }
 }
 // The operand itself; fp32: split into TF32 parts.
@@ -132,7 +132,9 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
 }
 
 // Launch that may begin while the kernel before it on the stream ends: every kernel launched so waits for
-// that one with griddepcontrol.wait before it touches memory, and lets its own successor begin at once.
+// that one with griddepcontrol.wait before it touches memory, and lets its own successor begin at once.  What
+// the one before may still write is read with plain loads: a read-only load is for data that no one writes
+// while the kernel is there.
 // With per-kernel profiling on, an event sits between the two and a plain launch is used.
 template <typename... P, typename... A>
 cudaError_t tq_launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs 
         const int n = (int)(min(r1, p0 + pass) - p0) * parts;
         // entry of a sequence's block j, and the slots of heads h .. h + VEC - 1 of token `off` of that block
         auto entry_of = [&](const Grown &g, const int32_t *table, int j) {
-          return !g.ok ? -1 : j >= g.have ? __ldg(a.free_blocks + g.at + (j - g.have)) : table[j];
+          return !g.ok ? -1 : j >= g.have ? a.free_blocks[g.at + (j - g.have)] : table[j];
         };
         auto slots_of = [&](const Grown &g, int32_t *table, int j, int off, int h, int64_t *to, int e) {
           if (off == 0 && h == 0 && g.ok && j >= g.have) table[j] = e;  // a new block begins with a new row
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(a.offsets + mid) / a.bs + 2 * (int64_t)mid <= u) lo = mid;
+    if (a.offsets[mid] / a.bs + 2 * (int64_t)mid <= u) lo = mid;
     else hi = mid;
   }
   const int b = lo;
