@@ -315,7 +315,7 @@ tq_status tq_search_topk(const tq_ctx *ctx, const void *q, tq_dtype dtype, int32
  * Paged caches: what a serving loop runs around them.  tq_page_extend makes block tables, lengths
  * and slot maps on the GPU (the `slots` of tq_encode_kv, the `new_slots` of tq_decode_step);
  * tq_append_kv, tq_block_scores and tq_attend_paged serve an uncompressed paged cache (the layers
- * that a user keeps in full precision, [ZC] 第六部分 "Boundary V"); tq_block_scores and
+ * that a user keeps in full precision, [ZC] "Boundary V"); tq_block_scores and
  * tq_select_blocks choose the blocks that one decode step reads, for tq_attend_paged and for
  * tq_attend_decode over the compressed cache alike.
  *
