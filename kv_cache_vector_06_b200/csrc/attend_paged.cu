@@ -11,7 +11,7 @@
 // block of four warps that share a row's steps (long rows) or a single warp (many short rows).  Each
 // warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
 // A row that falls to several workers leaves pieces (m, l, o) in the workspace, joined by a second
-// kernel.
+// kernel.  Where rows are few and short, a cluster of blocks takes each whole, in one launch.
 #include <algorithm>
 #include "paged_device.cuh"
 
@@ -288,6 +288,139 @@ struct Stream {
   }
 };
 
+// One warp's steps step0, step0 + apart, ... (n of them) of one row, through its ring: m, l and o of its lanes'
+// heads in `st`, l summed over the lanes of a head.
+template <typename T, int D, bool WIDE, int PARTS>
+__device__ __forceinline__ void stream_row(Stream<T, D, WIDE, PARTS> &st, const PagedArgs &a, int64_t row, const int32_t *table, int h,
+                                           int len, int step0, int n, int apart, unsigned ring, uint32_t *masks, unsigned qs, int warp,
+                                           int lane) {
+  using S = Shape<T, D>;
+  using St = Stream<T, D, WIDE, PARTS>;
+  const int esz_row = a.d * (int)sizeof(T);  // bytes of a row in the cache
+  const int dch = esz_row / 16;
+  const bool whole = a.bs % S::kTok == 0;  // a step lies in one block
+  const float sc = a.scale * kLog2e;
+  // block of this lane's token (of the whole step where it lies in one block)
+  auto entry = [&](int i) {
+    const int t = (step0 + i * apart) * S::kTok + (whole ? 0 : (lane & (S::kTok - 1)));
+    return i < n && t < len ? table[a.by_bs(t)] : -1;
+  };
+  auto issue = [&](int i, int e) {
+    const int stage = i % S::kStages;
+    const int t0 = (step0 + i * apart) * S::kTok;
+    const bool ok = e >= 0 && e < a.n_blocks;
+    const int t = t0 + (whole ? 0 : (lane & (S::kTok - 1)));
+    const int64_t off = ok ? (((int64_t)e * a.heads + h) * a.bs + (t - a.by_bs(t) * a.bs)) * esz_row : 0;
+    uint32_t valid = __ballot_sync(TQ_FULL_MASK, whole ? ok && t0 + lane < len : ok);
+    valid &= (1u << S::kTok) - 1u;
+    if (lane == 0) masks[stage] = valid;
+    const unsigned kb = ring + stage * S::kStage, vb = kb + S::kTok * S::kRow;
+#pragma unroll
+    for (int x = 0; x < S::kTok * S::kCh / 32; ++x) {
+      const int idx = lane + 32 * x, r = idx / S::kCh, ch = idx % S::kCh;
+      const int64_t base = whole ? off + r * esz_row : __shfl_sync(TQ_FULL_MASK, off, r);
+      const int64_t src = base + 16 * min(ch, dch - 1);  // inside the cache; read where the token is there
+      const int bytes = ((valid >> r) & 1u) && ch < dch ? 16 : 0;
+      cp16(kb + r * S::kRow + 16 * key_chunk(r, ch), static_cast<const char *>(a.k) + src, bytes);
+      cp16(vb + r * S::kRow + 16 * value_chunk<T>(r, ch), static_cast<const char *>(a.v) + src, bytes);
+    }
+  };
+  int e[S::kStages];
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
+  uint4 raw[St::kQ][St::kH];  // asked for before the rows, so that it does not queue behind them
+  if constexpr (St::kQInRegs) {
+#pragma unroll
+    for (int kg = 0; kg < St::kKg; ++kg) load_q<T, St::kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
+  }
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) {
+    if (i < n) issue(i, e[i]);
+    cp_commit();
+  }
+  int next = e[S::kStages - 1];
+  if constexpr (St::kQInRegs) {
+#pragma unroll
+    for (int kg = 0; kg < St::kKg; ++kg) make_q<T, St::kH>(st.qf[kg], raw[kg]);
+  }
+  if (qs != 0) {  // the block's warps share a row
+    for (int kg = warp; kg < St::kKg; kg += S::kWarps) St::put_q(a, row, qs, kg, lane);
+    __syncthreads();
+  }
+  st.clear();
+  for (int i = 0; i < n; ++i) {
+    cp_wait<S::kStages - 2>();
+    __syncwarp();  // this step's copies of every lane have landed; the last step's stage is free
+    if (i + S::kStages - 1 < n) issue(i + S::kStages - 1, next);
+    cp_commit();
+    next = entry(i + S::kStages);
+    const int stage = i % S::kStages;
+    const unsigned kb = ring + stage * S::kStage;
+    st.step(a, row, qs, kb, kb + S::kTok * S::kRow, masks[stage], sc, lane);
+  }
+  cp_wait<0>();
+  __syncwarp();
+#pragma unroll
+  for (int x = 0; x < St::kH; ++x) {
+    st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 1);
+    st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 2);
+  }
+}
+
+// Floats of a head's row in join_warps: padded, so that a warp's stores touch every bank once.
+template <typename T, int D>
+__host__ __device__ constexpr int padded_row() {
+  return D + (sizeof(T) == 2 ? 8 : 4);
+}
+
+// The warps' sums of one row joined in shared memory (`buf`, kWarps x 16 padded rows): done(head, channel, o of four
+// channels, m, l) for every head and four channels, spread over the block's threads.  Every warp's ring is drained.
+template <typename T, int D, bool WIDE, int PARTS, typename F>
+__device__ __forceinline__ void join_warps(const Stream<T, D, WIDE, PARTS> &st, const PagedArgs &a, float *buf, float (&mm)[Shape<T, D>::kWarps][16],
+                                           float (&ll)[Shape<T, D>::kWarps][16], int warp, int lane, F &&done) {
+  using St = Stream<T, D, WIDE, PARTS>;
+  constexpr int kWarps = Shape<T, D>::kWarps;
+  constexpr int kPad = padded_row<T, D>();
+  const int g = a.group;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < St::kH; ++x) {
+    const int hd = (lane >> 2) + 8 * x;
+    if (hd >= g) continue;
+    st.emit(buf + (warp * 16 + hd) * kPad, x, 1.f, D, lane);
+    if ((lane & 3) == 0) {
+      mm[warp][hd] = st.m[x];
+      ll[warp][hd] = st.l[x];
+    }
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < g * (D / 4); idx += 32 * kWarps) {
+    const int hd = idx / (D / 4), c = 4 * (idx % (D / 4));
+    if (c >= a.d) continue;
+    float top = -INFINITY, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mm[w][hd]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = mm[w][hd] == -INFINITY ? 0.f : exp2a(mm[w][hd] - top);
+      const float4 x = *reinterpret_cast<const float4 *>(buf + (w * 16 + hd) * kPad + c);
+      sum = fmaf(f, ll[w][hd], sum);
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
+    }
+    done(hd, c, v, top, sum);
+  }
+}
+template <typename O>
+__device__ __forceinline__ void put_out(O *out, const float4 &v, float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  store2(out, v.x * inv, v.y * inv);
+  store2(out + 2, v.z * inv, v.w * inv);
+}
+
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) attend_paged_kernel(PagedArgs a) {
   using S = Shape<T, D>;
@@ -329,10 +462,6 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
   int64_t unit = place[lead].unit - (int64_t)h * (steps + extra);  // place in the row, its cost in front
 
   const unsigned ring = smem_addr(smem) + warp * S::kRing;
-  const int esz_row = a.d * (int)sizeof(T);  // bytes of a row in the cache
-  const int dch = esz_row / 16;
-  const bool whole = a.bs % S::kTok == 0;  // a step lies in one block
-  const float sc = a.scale * kLog2e;
   const int rank = solo ? 0 : warp;
   St st;
 
@@ -354,72 +483,8 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
     const int64_t row = (int64_t)b * a.heads + h;
     const int32_t *table = a.table + (int64_t)b * a.max_blocks;
     const int n = (count - rank + team - 1) / team;
-    // block of this lane's token (of the whole step where it lies in one block)
-    auto entry = [&](int i) {
-      const int t = (first + rank + i * team) * S::kTok + (whole ? 0 : (lane & (S::kTok - 1)));
-      return i < n && t < len ? table[a.by_bs(t)] : -1;
-    };
-    auto issue = [&](int i, int e) {
-      const int stage = i % S::kStages;
-      const int t0 = (first + rank + i * team) * S::kTok;
-      const bool ok = e >= 0 && e < a.n_blocks;
-      const int t = t0 + (whole ? 0 : (lane & (S::kTok - 1)));
-      const int64_t off = ok ? (((int64_t)e * a.heads + h) * a.bs + (t - a.by_bs(t) * a.bs)) * esz_row : 0;
-      uint32_t valid = __ballot_sync(TQ_FULL_MASK, whole ? ok && t0 + lane < len : ok);
-      valid &= (1u << S::kTok) - 1u;
-      if (lane == 0) masks[warp][stage] = valid;
-      const unsigned kb = ring + stage * S::kStage, vb = kb + S::kTok * S::kRow;
-#pragma unroll
-      for (int x = 0; x < S::kTok * S::kCh / 32; ++x) {
-        const int idx = lane + 32 * x, r = idx / S::kCh, ch = idx % S::kCh;
-        const int64_t base = whole ? off + r * esz_row : __shfl_sync(TQ_FULL_MASK, off, r);
-        const int64_t src = base + 16 * min(ch, dch - 1);  // inside the cache; read where the token is there
-        const int bytes = ((valid >> r) & 1u) && ch < dch ? 16 : 0;
-        cp16(kb + r * S::kRow + 16 * key_chunk(r, ch), static_cast<const char *>(a.k) + src, bytes);
-        cp16(vb + r * S::kRow + 16 * value_chunk<T>(r, ch), static_cast<const char *>(a.v) + src, bytes);
-      }
-    };
-    int e[S::kStages];
-#pragma unroll
-    for (int i = 0; i < S::kStages; ++i) e[i] = entry(i);
-    uint4 raw[St::kQ][St::kH];  // asked for before the rows, so that it does not queue behind them
-    if constexpr (St::kQInRegs) {
-#pragma unroll
-      for (int kg = 0; kg < St::kKg; ++kg) load_q<T, St::kH>(raw[kg], a.q, row, a.group, a.d, kg, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      if (i < n) issue(i, e[i]);
-      cp_commit();
-    }
-    int next = e[S::kStages - 1];
-    if constexpr (St::kQInRegs) {
-#pragma unroll
-      for (int kg = 0; kg < St::kKg; ++kg) make_q<T, St::kH>(st.qf[kg], raw[kg]);
-    }
     const unsigned qs = St::kQInSmem && !solo ? smem_addr(smem) + S::kSmem : 0;
-    if (St::kQInSmem && !solo) {
-      for (int kg = warp; kg < St::kKg; kg += kWarps) St::put_q(a, row, qs, kg, lane);
-      __syncthreads();
-    }
-    st.clear();
-    for (int i = 0; i < n; ++i) {
-      cp_wait<S::kStages - 2>();
-      __syncwarp();  // this step's copies of every lane have landed; the last step's stage is free
-      if (i + S::kStages - 1 < n) issue(i + S::kStages - 1, next);
-      cp_commit();
-      next = entry(i + S::kStages);
-      const int stage = i % S::kStages;
-      const unsigned kb = ring + stage * S::kStage;
-      st.step(a, row, qs, kb, kb + S::kTok * S::kRow, masks[warp][stage], sc, lane);
-    }
-    cp_wait<0>();
-    __syncwarp();
-#pragma unroll
-    for (int x = 0; x < St::kH; ++x) {
-      st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 1);
-      st.l[x] += __shfl_xor_sync(TQ_FULL_MASK, st.l[x], 2);
-    }
+    stream_row<T, D, WIDE, PARTS>(st, a, row, table, h, len, first + rank, n, team, ring, masks[warp], qs, warp, lane);
 
     // ---- the row's end, or the worker's: the output, or a piece of it
     const bool starts = first == 0, ends = first + count == steps;
@@ -443,50 +508,18 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
         }
       }
     } else {
-      // padded rows: a warp's stores below touch every bank once
-      constexpr int kPad = D + (St::kBf ? 8 : 4);
-      float *buf = reinterpret_cast<float *>(smem);
-      __syncthreads();  // every warp's ring is drained: its shared memory holds the warps' sums now
-#pragma unroll
-      for (int x = 0; x < St::kH; ++x) {
-        const int hd = (lane >> 2) + 8 * x;
-        if (hd >= g) continue;
-        st.emit(buf + (warp * 16 + hd) * kPad, x, 1.f, D, lane);
-        if ((lane & 3) == 0) {
-          mm[warp][hd] = st.m[x];
-          ll[warp][hd] = st.l[x];
-        }
-      }
-      __syncthreads();
-      for (int idx = threadIdx.x; idx < g * (D / 4); idx += kThreads) {
-        const int hd = idx / (D / 4), c = 4 * (idx % (D / 4));
-        if (c >= a.d) continue;
-        float top = -INFINITY, sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mm[w][hd]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = mm[w][hd] == -INFINITY ? 0.f : exp2a(mm[w][hd] - top);
-          const float4 x = *reinterpret_cast<const float4 *>(buf + (w * 16 + hd) * kPad + c);
-          sum = fmaf(f, ll[w][hd], sum);
-          v.x = fmaf(f, x.x, v.x);
-          v.y = fmaf(f, x.y, v.y);
-          v.z = fmaf(f, x.z, v.z);
-          v.w = fmaf(f, x.w, v.w);
-        }
-        if (done) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          store2(out + hd * a.d + c, v.x * inv, v.y * inv);
-          store2(out + hd * a.d + c + 2, v.z * inv, v.w * inv);
-        } else {
-          *reinterpret_cast<float4 *>(piece + hd * a.d + c) = v;
-          if (c == 0) {
-            piece[g * a.d + hd] = top;
-            piece[g * a.d + g + hd] = sum;
-          }
-        }
-      }
+      join_warps<T, D, WIDE, PARTS>(st, a, reinterpret_cast<float *>(smem), mm, ll, warp, lane,
+                                    [&](int hd, int c, const float4 &v, float top, float sum) {
+                                      if (done) {
+                                        put_out(out + hd * a.d + c, v, sum);
+                                        return;
+                                      }
+                                      *reinterpret_cast<float4 *>(piece + hd * a.d + c) = v;
+                                      if (c == 0) {
+                                        piece[g * a.d + hd] = top;
+                                        piece[g * a.d + g + hd] = sum;
+                                      }
+                                    });
       __syncthreads();
     }
     if (starts && rank == 0 && lane == 0) {
@@ -496,6 +529,83 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
     }
     go_on();
   }
+}
+
+// Few short rows: a cluster of blocks takes one row whole, its warps the row's steps in turn, and joins its
+// blocks' sums through distributed shared memory: no scan, no pieces, one launch (8 rows of 1000 tokens: 9.0 us
+// per call against 11.0).
+template <typename T, int D, bool WIDE, int PARTS, typename O>
+__global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) attend_paged_rows_kernel(PagedArgs a, int blocks) {
+  using S = Shape<T, D>;
+  using St = Stream<T, D, WIDE, PARTS>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t masks[kWarps][S::kStages];
+  __shared__ float mm[kWarps][16], ll[kWarps][16];
+  __shared__ float2 ml[16];  // the block's m and l of each head
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int rank = blockIdx.x % blocks;
+  const int64_t row = blockIdx.x / blocks;
+  const int b = (int)(row / a.heads), h = (int)(row - (int64_t)b * a.heads), g = a.group;
+  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int steps = row_steps(len, a.max_len, S::kTok), step0 = rank * kWarps + warp, team = blocks * kWarps;
+  const int n = step0 < steps ? (steps - step0 + team - 1) / team : 0;
+  St st;
+  stream_row<T, D, WIDE, PARTS>(st, a, row, a.table + (int64_t)b * a.max_blocks, h, len, step0, n, team, smem_addr(smem) + warp * S::kRing,
+                                masks[warp], St::kQInSmem ? smem_addr(smem) + S::kSmem : 0, warp, lane);
+  float *buf = reinterpret_cast<float *>(smem), *sums = buf + kWarps * 16 * padded_row<T, D>();  // [16][D] behind the warps' rows
+  static_assert(sizeof(float) * 16 * (kWarps * padded_row<T, D>() + D) <= S::kSmem, "the block's sums fit behind its warps'");
+  O *out = static_cast<O *>(a.out) + row * g * a.d;
+  join_warps<T, D, WIDE, PARTS>(st, a, buf, mm, ll, warp, lane, [&](int hd, int c, const float4 &v, float top, float sum) {
+    if (blocks == 1) {
+      put_out(out + hd * a.d + c, v, sum);
+      return;
+    }
+    *reinterpret_cast<float4 *>(sums + hd * D + c) = v;
+    if (c == 0) ml[hd] = make_float2(top, sum);
+  });
+  if (blocks == 1) return;
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  // each block joins a share of the channels, the blocks' sums in their order
+  for (int idx = threadIdx.x * blocks + rank; idx < g * (D / 4); idx += kThreads * blocks) {
+    const int hd = idx / (D / 4), c = 4 * (idx % (D / 4));
+    if (c >= a.d) continue;
+    float m = -INFINITY, l = 0.f;
+    float2 pml[8];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f), po[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= blocks) break;
+      unsigned at_ml, at_o;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at_ml) : "r"(smem_addr(ml + hd)), "r"(i));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at_o) : "r"(smem_addr(sums + hd * D + c)), "r"(i));
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(pml[i].x), "=f"(pml[i].y) : "r"(at_ml) : "memory");
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                   : "=f"(po[i].x), "=f"(po[i].y), "=f"(po[i].z), "=f"(po[i].w)
+                   : "r"(at_o)
+                   : "memory");
+      m = fmaxf(m, pml[i].x);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= blocks) break;
+      const float f = pml[i].x == -INFINITY ? 0.f : exp2a(pml[i].x - m);
+      l = fmaf(f, pml[i].y, l);
+      o.x = fmaf(f, po[i].x, o.x);
+      o.y = fmaf(f, po[i].y, o.y);
+      o.z = fmaf(f, po[i].z, o.z);
+      o.w = fmaf(f, po[i].w, o.w);
+    }
+    put_out(out + hd * a.d + c, o, l);
+  }
+  // no block leaves while another still reads its shared memory
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 // Joins the pieces of rows that several workers shared: blocks (x, y), rows x, x + gridDim.x, ..., vectors of
@@ -557,12 +667,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(Paged
         for (int i = 1; i < groups; ++i) join(ml[tid + i * vecs].x, ml[tid + i * vecs].y, so[tid + i * vecs]);
       __syncthreads();
     }
-    if (grp == 0 && on) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      O *out = static_cast<O *>(a.out) + row * g * a.d + 4 * v;
-      store2(out, o.x * inv, o.y * inv);
-      store2(out + 2, o.z * inv, o.w * inv);
-    }
+    if (grp == 0 && on) put_out(static_cast<O *>(a.out) + row * g * a.d + 4 * v, o, l);
   }
 }
 
@@ -592,17 +697,41 @@ int most_workers(int device, int d) {
   return d <= 64 ? most_workers<64>(device) : d <= 128 ? most_workers<128>(device) : most_workers<256>(device);
 }
 
+// Steps of a warp up to which whole rows are taken where they fill less than half of the GPU, and twice as many
+// where they fill more.  Beyond, other blocks' bandwidth is worth the deal and the join.  us per call, whole
+// rows against dealt: bf16, 128 channels, 8 rows x 2000 tokens (4 steps) 9.8 / 12.0, x 4000 (8) 11.8 / 12.3;
+// 256 channels, 8 x 1000 (3) 10.9 / 12.3, x 2000 (6) 15.7 / 12.7; fp32, 128 channels, 8 x 1000 (4)
+// 9.9 / 12.0, x 2000 (8) 14.4 / 12.7; more than half full: bf16, 32 x 4096 (8) 16.7 / 19.7; fp32, 128 x 500 (8)
+// 18.8 / 26.0; bf16, 256 rows of 1 .. 500 (8) 12.3 / 17.0; 64 channels, 128 x 2000 (16) 19.8 / 20.8, but of
+// 1 .. 2000 17.0 / 14.5: whole rows do not even out lengths.
+template <typename T, int D>
+constexpr int kRowsSteps = sizeof(T) == 2 ? (D < 256 ? 8 : 4) : 512 / D;
+
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 cudaError_t launch(const PagedArgs &a, int device, cudaStream_t st) {
   using S = Shape<T, D>;
   constexpr int kSmem = Stream<T, D, WIDE, PARTS>::kSmem;
+  const int64_t rows = (int64_t)a.batch * a.heads, row_steps = a.max_len <= S::kTok ? 1 : (a.max_len - 1) / S::kTok + 1;
+  const int64_t room_rows = (int64_t)S::kOcc * tq_device_sms(device);
+  // whole rows, if each has room for a cluster at once and no warp has too many steps, however the lengths
+  // differ
+  int blocks = 8;
+  while (blocks > 1 && (rows * blocks > room_rows || row_steps <= blocks * S::kWarps / 2)) blocks /= 2;
+  const int most = kRowsSteps<T, D> * (2 * rows * blocks > room_rows ? 2 : 1);
+  if (rows * blocks <= room_rows && row_steps <= (int64_t)most * blocks * S::kWarps) {
+    auto kern = attend_paged_rows_kernel<T, D, WIDE, PARTS, O>;
+    cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), kSmem);
+    if (e != cudaSuccess) return e;
+    tq_prof_begin(TQK_ATTEND_PAGED, st);
+    e = tq_launch_clusters(kern, blocks, dim3((unsigned)(rows * blocks)), S::kThreads, kSmem, st, a, blocks);
+    tq_prof_end(TQK_ATTEND_PAGED, st);
+    return e;
+  }
   auto kern = attend_paged_kernel<T, D, WIDE, PARTS, O>;
   cudaError_t e = tq_smem_limit(reinterpret_cast<const void *>(kern), kSmem);
   if (e != cudaSuccess) return e;
   // as many blocks as fit on the GPU at once, fewer where the rows could not give each warp a step
-  const int64_t rows = (int64_t)a.batch * a.heads;
-  const int64_t steps = rows * (a.max_len <= S::kTok ? 1 : (a.max_len - 1) / S::kTok + 1);
-  const int grid = (int)std::min((steps + S::kWarps - 1) / S::kWarps, (int64_t)S::kOcc * tq_device_sms(device));
+  const int grid = (int)std::min((rows * row_steps + S::kWarps - 1) / S::kWarps, room_rows);
   tq_prof_begin(TQK_ATTEND_PAGED, st);
   e = tq_launch_dependent(kern, dim3((unsigned)grid), S::kThreads, kSmem, st, a);
   tq_prof_end(TQK_ATTEND_PAGED, st);

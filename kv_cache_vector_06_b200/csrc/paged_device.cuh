@@ -134,21 +134,34 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) {
 // Launch that may begin while the kernel before it on the stream ends: every kernel launched so waits for
 // that one with griddepcontrol.wait before it touches memory, and lets its own successor begin at once.  What
 // the one before may still write is read with plain loads: a read-only load is for data that no one writes
-// while the kernel is there.
+// while the kernel is there.  `blocks` above 1: in clusters of so many.
 // With per-kernel profiling on, an event sits between the two and a plain launch is used.
 template <typename... P, typename... A>
-cudaError_t tq_launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+cudaError_t tq_launch_clusters(void (*kern)(P...), int blocks, dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (!tq_prof_on()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (blocks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)blocks;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = tq_prof_on() ? 0 : 1;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... P, typename... A>
+cudaError_t tq_launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+  return tq_launch_clusters(kern, 1, grid, threads, smem, st, args...);
 }
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1: q = (mulhi(n, mul) + n) >> shift with

@@ -425,6 +425,9 @@ extern "C" tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_le
       !tq_aligned(free_blocks, 4) || !tq_aligned(free_head, 4) || !tq_aligned(free_head_out, 4) ||
       !tq_aligned(row_offsets, 8) || !tq_aligned(new_slots, 8))
     return tq_fail(TQ_EINVAL, "int32 arrays must be 4-byte and int64 arrays 8-byte aligned");
+  if (pages->batch > 0 && (seq_lens_out == new_lens || granted == seq_lens || granted == seq_lens_out ||
+                           seq_lens_out == free_blocks || granted == free_blocks))
+    return tq_fail(TQ_EINVAL, "seq_lens_out may be seq_lens and granted new_lens; no other arrays may be the same");
   DeviceScope dev_scope;
   st = dev_scope.enter(pages->device);
   if (st != TQ_OK) return st;

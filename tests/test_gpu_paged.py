@@ -324,6 +324,13 @@ def check_attend(tq, lens, n_kv, group, block, d, dtype, out_dtype=F32, seed=0, 
     err = np.abs(got - ref)
     assert np.all(err <= tol), f"{np.max(err[tol > 0] / tol[tol > 0])} of the tolerance, zeros {np.max(err[tol == 0], initial=0)}"
     assert np.all(got[[x == 0 for x in n]] == 0)
+    # the same rows under a bound on their lengths so large that they are dealt out in pieces
+    wide = np.concatenate([table, np.full((len(lens), -(-200000 // block)), -1)], axis=1)
+    cut = [min(x, max_len) for x in lens]
+    out = torch.full(q.shape, math.nan, dtype=out_dtype).cuda()
+    got2 = tq.attend_paged(tq.Pages(i32(wide), n_kv, block, n_blocks), i32(cut), wide.shape[1] * block, q.cuda(), kc.cuda(), vc.cuda(),
+                           scale=scale, out=out)
+    assert np.all(np.abs(got2.double().cpu().numpy() - ref) <= tol)
     return got
 
 
@@ -386,7 +393,7 @@ def test_attend_captured_calls_share_a_workspace(tq):
     d, block, group = 128, 16, 4
     ws = torch.full((1 << 24,), 255, dtype=torch.uint8).cuda()
     calls = []
-    for lens, n_kv in (([3000, 20, 700], 2), ([9000], 1), ([5, 4000, 0, 33] * 40, 4)):
+    for lens, n_kv in (([30000, 20, 700], 2), ([19000], 1), ([5, 4000, 0, 33] * 40, 4)):
         table, n_blocks = tables(lens, max(-(-n // block) for n in lens), block, seed=n_kv)
         kc, vc = (rows(n_blocks, n_kv, block, d, seed=s, dtype=BF16).cuda() for s in (1, 2))
         q, out = rows(len(lens), n_kv * group, d, seed=3, dtype=BF16).cuda(), torch.empty(len(lens), n_kv * group, d).cuda()

@@ -22,8 +22,8 @@ def pages(lib, **over):
 
 
 def extend(lib, pg, **over):
-    a = dict(seq_lens=P, new_lens=P, free=P, n_free=10, head=P, lens_out=P, granted=P, head_out=P, offsets=P, slots=P,
-             n_slots=6) | over
+    a = dict(seq_lens=P, new_lens=2 * P, free=3 * P, n_free=10, head=P, lens_out=4 * P, granted=5 * P, head_out=P, offsets=P,
+             slots=P, n_slots=6) | over
     return lib.LIB.tq_page_extend(pg, *a.values(), None)
 
 
@@ -71,7 +71,9 @@ def test_empty_batch_is_no_work(lib):
 @pytest.mark.parametrize("over", [dict(seq_lens=None), dict(new_lens=None), dict(free=None), dict(head=None),
                                   dict(lens_out=None), dict(granted=None), dict(head_out=None), dict(offsets=None),
                                   dict(slots=None), dict(n_free=-1), dict(n_slots=-2), dict(n_slots=5), dict(seq_lens=P + 1),
-                                  dict(offsets=P + 4), dict(slots=P + 4), dict(head=P + 2)])
+                                  dict(offsets=P + 4), dict(slots=P + 4), dict(head=P + 2),
+                                  dict(lens_out=2 * P), dict(granted=P), dict(granted=4 * P), dict(lens_out=3 * P),
+                                  dict(granted=3 * P)])
 def test_extend_refusals(lib, over):
     assert extend(lib, pages(lib), **over) == EINVAL and lib.LIB.tq_last_error()
 
