@@ -6,7 +6,7 @@
 // group's query heads share each row read, so the products run on the tensor cores (mma.sync: the
 // 128-row tiles of tcgen05 would hold at most 16 query heads), and the loads never wait for them.
 //
-// Work is counted in steps of TOK tokens over all (sequence, KV head) rows laid end to end; every worker
+// Work is counted in steps of 16 tokens (fp32 rows of more than 64 channels: 8) over all (sequence, KV head) rows laid end to end; every worker
 // takes an equal run of steps, so a ragged batch ends at one time whatever its lengths.  A worker is a
 // block of four warps that share a row's steps (long rows) or a single warp (many short rows).  Each
 // warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
@@ -32,10 +32,10 @@ struct PagedArgs {
 // What a row costs a worker beside its steps (its queries, its first loads, the joining of the warps), in
 // steps of the worker: as long as 64 KB (a block) or 16 KB (a warp) of the cache take it.  Without it a block
 // that drew several short rows ended last: 7 sequences of 1 to 9999 tokens x 4 heads took 47 us, with it 35.
-template <int D>
-constexpr int kTeamRowCost = 1024 / D;
-template <int D>
-constexpr int kSoloRowCost = 256 / D;
+template <typename T, int D>
+constexpr int kTeamRowCost = 65536 / Shape<T, D>::kStage;
+template <typename T, int D>
+constexpr int kSoloRowCost = 16384 / Shape<T, D>::kStage;
 
 // Floats of one piece, a multiple of four.
 __host__ __device__ __forceinline__ int piece_floats(int group, int d) { return (group * (d + 2) + 3) & ~3; }
@@ -104,9 +104,9 @@ struct Stream {
     const int c = lane & 3, r = lane >> 2;
     // chunk 4 kg + c of token r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
     const unsigned at[2] = {(unsigned)(r * S::kRow + 16 * key_chunk(r, c)), (unsigned)(r * S::kRow + 16 * key_chunk(r, 4 + c))};
-    float s[kBf ? kT : 2][4];  // fp32: two sums, of every other group, so that the products wait less for one another
+    float s[2][4];  // of one tile of 8 tokens: two sums, of every other group, so that the products wait less
 #pragma unroll
-    for (int t = 0; t < (kBf ? kT : 2); ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
@@ -136,18 +136,18 @@ struct Stream {
             split_tf32_cut(k[2 * u], h0, l0);
             split_tf32_cut(k[2 * u + 1], h1, l1);
             if constexpr (WIDE) {
-              mma_tf32(s[kg & 1], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
-              mma_tf32(s[kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
-              mma_tf32(s[kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
+              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
+              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
+              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
             } else {
-              mma_tf32(s[kg & 1], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
-              mma_tf32(s[kg & 1], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
+              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
+              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
             }
           }
         }
       }
     }
-    if constexpr (!kBf) {
+    if constexpr (kT == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
     }
@@ -233,33 +233,38 @@ struct Stream {
         }
       }
     } else {
-      // left operand: column c is token 2 c, column c + 4 token 2 c + 1
-      uint32_t ph[kH][2], pl[kH][2];
+      // left operand of tile t: column c is token 8 t + 2 c, column c + 4 token 8 t + 2 c + 1
+      uint32_t ph[kT][kH][2], pl[kT][kH][2];
 #pragma unroll
-      for (int x = 0; x < kH; ++x)
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) split_tf32(__float_as_uint(p[x][0][i]), ph[x][i], pl[x][i]);
+        for (int x = 0; x < kH; ++x)
 #pragma unroll
-      for (int g = 0; g < kNt / 4; ++g) {
-        uint32_t v0[4], v1[4];  // four channels of tokens 2 c and 2 c + 1, one per tile
-        lds128(v0, vbase + (2 * c) * S::kRow + 16 * value_chunk<T>(2 * c, 8 * g + r));
-        lds128(v1, vbase + (2 * c + 1) * S::kRow + 16 * value_chunk<T>(2 * c + 1, 8 * g + r));
+          for (int i = 0; i < 2; ++i) split_tf32(__float_as_uint(p[x][t][i]), ph[t][x][i], pl[t][x][i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t h0, l0, h1, l1;
-          split_tf32_cut(v0[i], h0, l0);
-          split_tf32_cut(v1[i], h1, l1);
-          float(&acc)[4] = o[4 * g + i];
-          if constexpr (WIDE) {
-            mma_tf32(acc, pl[0][0], pl[kH - 1][0], pl[0][1], pl[kH - 1][1], h0, h1);
-            mma_tf32(acc, ph[0][0], ph[kH - 1][0], ph[0][1], ph[kH - 1][1], l0, l1);
-            mma_tf32(acc, ph[0][0], ph[kH - 1][0], ph[0][1], ph[kH - 1][1], h0, h1);
-          } else {
-            mma_tf32(acc, 0u, ph[0][0], 0u, ph[0][1], l0, l1);
-            mma_tf32(acc, ph[0][0], pl[0][0], ph[0][1], pl[0][1], h0, h1);
+      for (int g = 0; g < kNt / 4; ++g)
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          const int tok = 8 * t + 2 * c;
+          uint32_t v0[4], v1[4];  // four channels of tokens 8 t + 2 c and 8 t + 2 c + 1, one per tile of o
+          lds128(v0, vbase + tok * S::kRow + 16 * value_chunk<T>(tok, 8 * g + r));
+          lds128(v1, vbase + (tok + 1) * S::kRow + 16 * value_chunk<T>(tok + 1, 8 * g + r));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h0, l0, h1, l1;
+            split_tf32_cut(v0[i], h0, l0);
+            split_tf32_cut(v1[i], h1, l1);
+            float(&acc)[4] = o[4 * g + i];
+            if constexpr (WIDE) {
+              mma_tf32(acc, pl[t][0][0], pl[t][kH - 1][0], pl[t][0][1], pl[t][kH - 1][1], h0, h1);
+              mma_tf32(acc, ph[t][0][0], ph[t][kH - 1][0], ph[t][0][1], ph[t][kH - 1][1], l0, l1);
+              mma_tf32(acc, ph[t][0][0], ph[t][kH - 1][0], ph[t][0][1], ph[t][kH - 1][1], h0, h1);
+            } else {
+              mma_tf32(acc, 0u, ph[t][0][0], 0u, ph[t][0][1], l0, l1);
+              mma_tf32(acc, ph[t][0][0], pl[t][0][0], ph[t][0][1], pl[t][0][1], h0, h1);
+            }
           }
         }
-      }
     }
   }
 
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
   // ---- workers
   const int64_t rows = (int64_t)a.batch * a.heads;
   const bool solo = rows >= (int64_t)gridDim.x && scan.total < 8 * rows;
-  const int team = solo ? 1 : kWarps, extra = solo ? kSoloRowCost<D> : kTeamRowCost<D>;
+  const int team = solo ? 1 : kWarps, extra = solo ? kSoloRowCost<T, D> : kTeamRowCost<T, D>;
   const int64_t workers = max((int64_t)1, min((int64_t)gridDim.x * (solo ? kWarps : 1), scan.total / (solo ? 1 : kWarps)));
   const Deal deal(scan.total + rows * extra, workers);
   for (int w = 0; w < kWarps; w += team) {
@@ -705,7 +710,7 @@ int most_workers(int device, int d) {
 // 18.8 / 26.0; bf16, 256 rows of 1 .. 500 (8) 12.3 / 17.0; 64 channels, 128 x 2000 (16) 19.8 / 20.8, but of
 // 1 .. 2000 17.0 / 14.5: whole rows do not even out lengths.
 template <typename T, int D>
-constexpr int kRowsSteps = sizeof(T) == 2 ? (D < 256 ? 8 : 4) : 512 / D;
+constexpr int kRowsSteps = sizeof(T) == 2 ? (D < 256 ? 8 : 4) : 32768 / Shape<T, D>::kStage;
 
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 cudaError_t launch(const PagedArgs &a, int device, cudaStream_t st) {

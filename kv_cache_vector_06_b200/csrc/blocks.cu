@@ -109,7 +109,7 @@ struct Scorer<float, D, WIDE> {
   using S = Shape<float, D>;
   static constexpr int kLanes = D == 64 ? 16 : 32;  // lanes of a row
   static constexpr int kAt = 32 / kLanes;           // blocks at once
-  static constexpr int kEach = 8 / kAt;             // blocks of a lane
+  static constexpr int kEach = 8 / kAt;             // blocks of a lane, of eight
   static constexpr int kVec = D == 256 ? 2 : 1;
   static constexpr int kHeads = WIDE ? 16 : 8;
   static constexpr bool kQInRegs = kHeads * kVec <= 16;  // else four heads at a time, from the cache
@@ -133,6 +133,17 @@ struct Scorer<float, D, WIDE> {
   __device__ __forceinline__ void prepare() {}
   static __device__ __forceinline__ float pick(float x, float lo, float hi, float s) { return fmaf(x, x >= 0.f ? hi : lo, s); }
   __device__ __forceinline__ float step(const BlockScoreArgs &a, int64_t row, unsigned lower, unsigned upper, int lane, int &k) {
+    const int v = lane % kLanes;
+    float mine = -INFINITY;
+    for (int half = 0; half < S::kTok / 8; ++half, lower += 8 * S::kRow, upper += 8 * S::kRow) {
+      const float x = eight(a, row, lower, upper, lane);
+      if (v / kEach == half) mine = x;
+    }
+    k = v < kEach * (S::kTok / 8) ? 8 * (v / kEach) + lane / kLanes + kAt * (v % kEach) : -1;
+    return mine;
+  }
+  // The score of block lane / kLanes + kAt (v % kEach) of eight.
+  __device__ __forceinline__ float eight(const BlockScoreArgs &a, int64_t row, unsigned lower, unsigned upper, int lane) {
     const int v = lane % kLanes;
     float best = -INFINITY;
 #pragma unroll
@@ -174,7 +185,6 @@ struct Scorer<float, D, WIDE> {
       for (int o = kEach; o < kLanes; o <<= 1) x = fmaxf(x, __shfl_xor_sync(TQ_FULL_MASK, x, o));
       best = fmaxf(best, x);
     }
-    k = v < kEach ? lane / kLanes + kAt * v : -1;
     return best;
   }
 };

@@ -4,18 +4,19 @@
 
 #include "device_common.cuh"
 
-// Rows of d padded to D channels; T the cache's type.  A step's keys and values take 64 D bytes of ring.  At
+// Rows of d padded to D channels; T the cache's type.  A step's keys and values take 4 to 16 KB of ring.  At
 // least two blocks share an SM, so that one streams while the other begins a row or joins its warps, with
 // two to three steps of each warp in flight and as many registers as the tiles need.  Measured (32 sequences of
 // up to 2000 tokens x 8 heads of 256 channels, bf16): 3 warps x 2 blocks 58 us, 6 x 1 69 us; (up to 4000
 // tokens of 128 channels) 4 x 2 50 us, 8 x 1 58 us, 3 x 3 54 us, two stages instead of three 52 us; (up to
-// 8000 of 64) 4 x 3 51 us, 4 x 2 54 us; (7 x 9999 tokens of 64, fp32) 4 x 2 24.7 us, 4 x 3 27.8 us.
+// 8000 of 64) 4 x 3 51 us, 4 x 2 54 us; (7 x 9999 tokens of 64, fp32) 4 x 2 24.7 us, 4 x 3
+// 27.8 us; steps of 16 tokens there instead of 8 (two independent chains) 96 us instead of 105 for 32 x 8000.
 template <typename T, int D>
 struct Shape {
-  static constexpr int kTok = 32 / sizeof(T);             // tokens per step: 16 (bf16) or 8 (fp32)
+  static constexpr int kTok = sizeof(T) == 2 || D == 64 ? 16 : 8;  // tokens per step
   static constexpr int kRow = D * (int)sizeof(T);         // bytes of a padded row
   static constexpr int kCh = kRow / 16;                   // 16-byte chunks of a row
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kStages = D == 64 && sizeof(T) == 2 ? 4 : D <= 128 ? 3 : 2;
   static constexpr int kWarps = D == 256 ? 3 : 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOcc = D == 64 && sizeof(T) == 2 ? 3 : 2;  // blocks per SM
