@@ -12,7 +12,7 @@
 // warp streams its steps through a ring of its own (cp.async, no block barrier) with its own m, l and o.
 // A row that falls to several workers leaves pieces (m, l, o) in the workspace, joined by a second
 // kernel.  A ragged batch of 64 sequences of 1024 .. 32768 tokens x 8 KV heads of 128 bf16 channels (4.4 GB):
-// 642-660 us, 6.7-6.9 TB/s.  Where rows are few and short, a cluster of blocks takes each whole, in one launch.
+// 645-660 us, 6.7-6.9 TB/s.  Where rows are few and short, a cluster of blocks takes each whole, in one launch.
 #include <algorithm>
 #include "paged_device.cuh"
 
@@ -59,7 +59,7 @@ struct Stream {
   static constexpr int kQ = kQInRegs ? kKg : 1;
   // Queries that the registers do not hold lie in shared memory, once for the block's warps, in the order in
   // which the lanes take them; where a warp works alone, or where they would cost the second block of the SM,
-  // each step asks the first-level cache for them (32 x 8 heads of 256 channels, fp32: 138 us, from the cache 172).
+  // each step asks the first-level cache for them (32 x 8 heads of 256 channels, fp32: 160 us, from the cache 195).
   static constexpr int kQBytes = kKg * (WIDE ? 2 : 1) * (kBf ? 1 : 2) * 512;
   static constexpr bool kQInSmem = !kQInRegs && kQBytes <= 16384;
   static constexpr int kSmem = S::kSmem + (kQInSmem ? kQBytes : 0);
@@ -69,6 +69,12 @@ struct Stream {
   float o[kNt][4], m[kH], l[kH];
   uint32_t qf[kQ][kH][kBf ? 1 : 2][4];
 
+  // A tensor core cuts what it returns: summed there, step after step, o shrank by up to 5e-6 of itself over
+  // 20000 tokens.  So each step's products are summed apart and added here, rounded to nearest.
+  static __device__ __forceinline__ void add(float (&to)[4], const float (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] += x[i];
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < kNt; ++n)
@@ -105,9 +111,9 @@ struct Stream {
     const int c = lane & 3, r = lane >> 2;
     // chunk 4 kg + c of token r lies at at[kg & 1] + 128 (kg / 2): key_chunk swaps the groups of odd rows
     const unsigned at[2] = {(unsigned)(r * S::kRow + 16 * key_chunk(r, c)), (unsigned)(r * S::kRow + 16 * key_chunk(r, 4 + c))};
-    float s[2][4];  // of one tile of 8 tokens: two sums, of every other group, so that the products wait less
+    float s[kT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
 #pragma unroll
@@ -127,6 +133,7 @@ struct Stream {
       for (int t = 0; t < kT; ++t) {
         uint32_t k[4];
         lds128(k, kbase + at[kg & 1] + 8 * t * S::kRow + 128 * (kg >> 1));
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};  // fp32: one group's products, added as in add()
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           if constexpr (kBf) {
@@ -137,20 +144,17 @@ struct Stream {
             split_tf32_cut(k[2 * u], h0, l0);
             split_tf32_cut(k[2 * u + 1], h1, l1);
             if constexpr (WIDE) {
-              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
-              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
-              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
+              mma_tf32(acc, f[0][1][2 * u], f[1][1][2 * u], f[0][1][2 * u + 1], f[1][1][2 * u + 1], h0, h1);
+              mma_tf32(acc, f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], l0, l1);
+              mma_tf32(acc, f[0][0][2 * u], f[1][0][2 * u], f[0][0][2 * u + 1], f[1][0][2 * u + 1], h0, h1);
             } else {
-              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
-              mma_tf32(s[kT == 2 ? t : kg & 1], f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
+              mma_tf32(acc, f[0][0][2 * u], 0u, f[0][0][2 * u + 1], 0u, l0, l1);
+              mma_tf32(acc, f[0][0][2 * u], f[0][1][2 * u], f[0][0][2 * u + 1], f[0][1][2 * u + 1], h0, h1);
             }
           }
         }
+        if constexpr (!kBf) add(s[t], acc);
       }
-    }
-    if constexpr (kT == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
     }
     // logits in units of log2, masked; lane: head r (+ 8), tokens 8 t + 2 c, 8 t + 2 c + 1
     float p[kH][kT][2];
@@ -223,14 +227,16 @@ struct Stream {
         ldsm4t(v, vbase + (lane & 15) * S::kRow + 16 * value_chunk<T>(lane & 15, n + (lane >> 4)));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
           if constexpr (WIDE) {
 #pragma unroll
             for (int i = PARTS - 1; i >= 0; --i)
-              mma_bf16(o[n + u], w[i][0][0], w[i][kH - 1][0], w[i][0][1], w[i][kH - 1][1], v[2 * u], v[2 * u + 1]);
+              mma_bf16(acc, w[i][0][0], w[i][kH - 1][0], w[i][0][1], w[i][kH - 1][1], v[2 * u], v[2 * u + 1]);
           } else {
-            if constexpr (PARTS == 3) mma_bf16(o[n + u], 0u, w[PARTS - 1][0][0], 0u, w[PARTS - 1][0][1], v[2 * u], v[2 * u + 1]);
-            mma_bf16(o[n + u], w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], v[2 * u], v[2 * u + 1]);
+            if constexpr (PARTS == 3) mma_bf16(acc, 0u, w[PARTS - 1][0][0], 0u, w[PARTS - 1][0][1], v[2 * u], v[2 * u + 1]);
+            mma_bf16(acc, w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], v[2 * u], v[2 * u + 1]);
           }
+          add(o[n + u], acc);
         }
       }
     } else {
@@ -255,7 +261,7 @@ struct Stream {
             uint32_t h0, l0, h1, l1;
             split_tf32_cut(v0[i], h0, l0);
             split_tf32_cut(v1[i], h1, l1);
-            float(&acc)[4] = o[4 * g + i];
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (WIDE) {
               mma_tf32(acc, pl[t][0][0], pl[t][kH - 1][0], pl[t][0][1], pl[t][kH - 1][1], h0, h1);
               mma_tf32(acc, ph[t][0][0], ph[t][kH - 1][0], ph[t][0][1], ph[t][kH - 1][1], l0, l1);
@@ -264,6 +270,7 @@ struct Stream {
               mma_tf32(acc, 0u, ph[t][0][0], 0u, ph[t][0][1], l0, l1);
               mma_tf32(acc, ph[t][0][0], pl[t][0][0], ph[t][0][1], pl[t][0][1], h0, h1);
             }
+            add(o[4 * g + i], acc);
           }
         }
     }
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) atte
 }
 
 // Few short rows: a cluster of blocks takes one row whole, its warps the row's steps in turn, and joins its
-// blocks' sums through distributed shared memory: no scan, no pieces, one launch (8 rows of 1000 tokens: 9.0 us
+// blocks' sums through distributed shared memory: no scan, no pieces, one launch (8 rows of 1000 tokens: 8.9 us
 // per call against 11.0).
 template <typename T, int D, bool WIDE, int PARTS, typename O>
 __global__ void __launch_bounds__(Shape<T, D>::kThreads, Shape<T, D>::kOcc) attend_paged_rows_kernel(PagedArgs a, int blocks) {

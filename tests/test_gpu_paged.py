@@ -349,6 +349,22 @@ def test_attend_lengths(tq, dtype, lens):
     check_attend(tq, lens, 2, 4, 16, 128, dtype, seed=len(lens) + lens[0])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_long_sums_do_not_shrink(tq, dtype):
+    """Equal weights over values of one sign, some 120 steps per warp: sums rounded to nearest stay within a few
+    roundings (2^-24 x sqrt(120) x 4, and 8 cuts of 2^-23 inside a step: 3.6e-6 at the very most, 1e-6 as it comes);
+    a sum cut at each step loses half of 2^-23 every time, 7e-6."""
+    batch, n_kv, d, block, n = 16, 8, 64, 16, 20000
+    table = torch.randperm(batch * n // block, generator=torch.Generator().manual_seed(1)).view(batch, -1).to(torch.int32)
+    v = (torch.rand(batch * n // block, n_kv, block, d, generator=torch.Generator("cuda").manual_seed(2), device="cuda") + 1).to(dtype)
+    pages = tq.Pages(table.cuda(), n_kv, block, batch * n // block)
+    q = torch.zeros(batch, 2 * n_kv, d, dtype=dtype).cuda()
+    got = tq.attend_paged(pages, i32([n] * batch), n, q, torch.zeros_like(v), v).double()
+    ref = v[table.long().cuda()].double().mean((1, 3)).repeat_interleave(2, dim=1)
+    err = (got - ref) / ref
+    assert err.abs().max() <= 3.6e-6 and err.mean().abs() <= 1.5e-6, (err.abs().max(), err.mean())
+
+
 def test_attend_many_sequences(tq):
     """More rows than the GPU has room for at once, ragged."""
     rng = np.random.default_rng(0)
