@@ -59,7 +59,8 @@ struct Stream {
   static constexpr int kQ = kQInRegs ? kKg : 1;
   // Queries that the registers do not hold lie in shared memory, once for the block's warps, in the order in
   // which the lanes take them; where a warp works alone, or where they would cost the second block of the SM,
-  // each step asks the first-level cache for them (32 x 8 heads of 256 channels, fp32: 160 us, from the cache 195).
+  // each step asks the first-level cache for them (32 x 8 heads of 256 channels, fp32: 138 us, from the cache
+  // 172, measured before the sums of add(); with them 160).
   static constexpr int kQBytes = kKg * (WIDE ? 2 : 1) * (kBf ? 1 : 2) * 512;
   static constexpr bool kQInSmem = !kQInRegs && kQBytes <= 16384;
   static constexpr int kSmem = S::kSmem + (kQInSmem ? kQBytes : 0);
