@@ -369,7 +369,8 @@ tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_lens, const i
  * of every key channel per (block, KV head): the bounds that tq_block_scores reads.
  * Sequence b's rows row_offsets[b] .. row_offsets[b] + granted[b] - 1 are its tokens
  * seq_lens[b] - granted[b] .. seq_lens[b] - 1, as tq_page_extend leaves them.
- *   seq_lens, granted, row_offsets  device, as written by tq_page_extend (lengths after the append)
+ *   seq_lens, granted, row_offsets  device, as written by tq_page_extend (lengths after the append), or
+ *                     a run of those sequences: rows in order, the first anywhere in k_new and v_new
  *   k_new, v_new      device rows of dtype: head h of row r at r * ld + h * d elements (16-byte
  *                     aligned, ld a multiple of 16 bytes, ld >= n_kv_heads * d)
  *   n_rows            rows of k_new and v_new; sequences whose rows pass it are not appended

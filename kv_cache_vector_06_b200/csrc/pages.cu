@@ -310,7 +310,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv_kernel(AppendArgs
   const int add = a.granted[b], len = a.lens[b];
   if (add <= 0 || len < add || len > (int64_t)a.max_blocks * a.bs || row0 < 0 || row0 + add > a.n_rows) return;
   const int before = len - add;
-  const int64_t j = before / a.bs + (u - (row0 / a.bs + 2 * (int64_t)b));
+  const int64_t nth = u - (row0 / a.bs + 2 * (int64_t)b);
+  if (nth < 0) return;  // in front of the first sequence's rows
+  const int64_t j = before / a.bs + nth;
   if (j > (len - 1) / a.bs) return;
   const int e = a.table[(int64_t)b * a.max_blocks + j];
   if (e < 0 || e >= a.n_blocks) return;

@@ -173,6 +173,15 @@ def test_append_refused_rows_and_bounds_only(tq):
     append_case(tq, [40, 0, 48, 30], [33, 0, 48, 20], 2, 16, 64, F32, seed=6, table=table)
 
 
+@pytest.mark.parametrize("first", [1, 16, 40, 333])
+def test_append_rows_that_begin_later(tq, first):
+    """The later sequences of a batch alone: their first row lies behind rows of k_new that nobody appends."""
+    lens, granted = [100, 17, 64], [20, 1, 64]
+    off = first + np.concatenate([[0], np.cumsum(granted)])
+    for dtype, n_kv in ((BF16, 2), (F32, 9)):
+        append_case(tq, lens, granted, n_kv, 16, 128, dtype, seed=first, offsets=off)
+
+
 # ------------------------------------------------------------------------------------ block_scores
 def check_scores(tq, lens, n_kv, group, block, d, dtype, seed, width=None, table=None):
     if table is None:
