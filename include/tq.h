@@ -378,6 +378,7 @@ tq_status tq_page_extend(const tq_pages *pages, const int32_t *seq_lens, const i
  *                     beside a compressed cache)
  *   bounds            device [n_blocks][n_kv_heads][2][d] of dtype, lower then upper, or NULL.  A block
  *                     that begins with a new token starts afresh; another one's bounds are widened.
+ *                     NaN is passed over where a channel holds anything else.
  * No block may hold new tokens of two sequences.
  * d a multiple of 8 in [8, 256].
  * Errors: TQ_EINVAL (nulls, shapes, alignment), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
@@ -418,7 +419,9 @@ tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_lens, const
 
 /* Attention of one new token per sequence over an uncompressed paged cache:
  *   out[b][hq] = sum_t softmax_t(scale <q[b][hq], k_t>) v_t  over tokens t < seq_lens[b] of KV head
- *   hq / (n_q_heads / n_kv_heads); zeros where no token is left.
+ *   hq / (n_q_heads / n_kv_heads); zeros where no token is left.  NaN in a query, a key or a value that
+ *   the sum reads comes out as NaN, and so may an infinity; what lies behind a sequence's tokens is
+ *   not read.
  *   max_seq_len  host-known upper bound of seq_lens (larger values are clamped to it), at most
  *                max_blocks * block_size
  *   q            device [batch][n_q_heads][d] of dtype

@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(Paged
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto join = [&](float pm, float pl, const float4 &po) {
-      if (pm == -INFINITY) return;
+      if (pm == -INFINITY && pl == 0.f) return;  // no token; one whose logits are all NaN passes them on
       const float to = fmaxf(m, pm), f0 = exp2a(m - to), f1 = exp2a(pm - to);
       m = to;
       l = l * f0 + pl * f1;
@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_paged_merge_kernel(Paged
       for (int i = 0; i < 4; ++i) {
         const int p = p0 + i * groups;
         pm[i] = -INFINITY;
+        pl[i] = 0.f;
         if (p < n) {
           // a worker's two pieces: of a row that began before it, and of the row that it begins
           const float *piece = a.piece + ((int64_t)(own.x + p * apart) * 2 + (p == 0 ? 1 : 0)) * stride;

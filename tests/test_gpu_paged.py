@@ -374,6 +374,29 @@ def test_attend_long_sums_do_not_shrink(tq, dtype):
     assert err.abs().max() <= 3.6e-6 and err.mean().abs() <= 1.5e-6, (err.abs().max(), err.mean())
 
 
+@pytest.mark.parametrize("dtype,d,group", [(BF16, 128, 4), (F32, 64, 4), (F32, 128, 16), (BF16, 64, 16)])
+@pytest.mark.parametrize("lens", [[9999, 12000, 16], [300, 500, 16]])
+def test_attend_passes_nan_on(tq, dtype, d, group, lens):
+    """NaN in one head's query, in one token's key of one KV head and in one value: exactly the outputs that
+    read them are NaN, for rows that several blocks share and for whole ones, and the others are as without."""
+    n_kv, block = 2, 16
+    table, n_blocks = tables(lens, -(-max(lens) // block), block, seed=4)
+    q, k, v = (rows(*s, seed=i, dtype=dtype).cuda() for i, s in
+               enumerate([(3, n_kv * group, d), (n_blocks, n_kv, block, d), (n_blocks, n_kv, block, d)]))
+    pages = tq.Pages(i32(table), n_kv, block, n_blocks)
+    clean = tq.attend_paged(pages, i32(lens), max(lens), q, k, v)
+    assert clean.isfinite().all()
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    q[0, 1, 3] = math.nan
+    bad[0, 1] = True
+    k[int(table[1][200 // block]), 1, 200 % block, 5] = math.nan
+    bad[1, group:] = True
+    v[int(table[2][0]), 0, 7, d - 1] = math.nan
+    bad[2, :group, d - 1] = True
+    got = tq.attend_paged(pages, i32(lens), max(lens), q, k, v)
+    assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], clean[~bad])
+
+
 def test_attend_many_sequences(tq):
     """More rows than the GPU has room for at once, ragged."""
     rng = np.random.default_rng(0)
