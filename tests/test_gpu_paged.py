@@ -182,6 +182,23 @@ def test_append_rows_that_begin_later(tq, first):
         append_case(tq, lens, granted, n_kv, 16, 128, dtype, seed=first, offsets=off)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [8, 128, 256])
+def test_append_bounds_pass_over_nan(tq, dtype, d):
+    """A channel's bounds are those of its other values, and NaN where it has none."""
+    k = rows(40, 2, d, seed=d, dtype=dtype).cuda()
+    k[0, 0, 0] = k[39, 0, 1] = math.nan
+    k[5, 1] = math.nan
+    k[16:32, 0, 3] = math.nan
+    pages = tq.Pages(i32([[0, 1, 2]]), 2, 16, 3)
+    bd = torch.zeros(3, 2, 2, d, dtype=dtype).cuda()
+    tq.append_kv(pages, i32([40]), i32([40]), torch.tensor([0, 40]).cuda(), k, bounds=bd)
+    for j in range(3):
+        x = k[16 * j:16 * j + 16].double().cpu().numpy()
+        ref = np.stack([np.fmin.reduce(x, axis=0), np.fmax.reduce(x, axis=0)], axis=1)
+        np.testing.assert_array_equal(bd[j].double().cpu().numpy(), ref)
+
+
 # ------------------------------------------------------------------------------------ block_scores
 def check_scores(tq, lens, n_kv, group, block, d, dtype, seed, width=None, table=None):
     if table is None:
