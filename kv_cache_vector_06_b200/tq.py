@@ -473,10 +473,17 @@ def _raw_stream(device: int, stream) -> int:
 
 
 def _new(shape, dtype, device, stream):
-    """A tensor that a call makes for itself: kept from reuse while the call's own stream still works on it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor that a call makes for itself.  On a given stream it comes from that stream's own memory: a block of
+    the current stream's may still be in use by what is queued there, which the given stream does not wait for.  The
+    current stream, where the caller goes on, keeps it from reuse too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
     return t
 
 

@@ -632,6 +632,43 @@ def test_calls_on_a_given_stream(tq):
         assert torch.equal(x, y)
 
 
+def test_calls_on_a_given_stream_leave_queued_work_alone(tq):
+    """stream= while the current stream still holds queued reads and writes of memory that it has freed: what the calls
+    make for themselves is none of it.  Sizes are those of their outputs and workspace."""
+    n_kv, group, d, block, batch, keep = 2, 4, 128, 16, 3, 7
+    n = [20000, 700, 3000]
+    table, n_blocks = tables(n, 1250, block, 3)
+    pages, lens, side = tq.Pages(i32(table), n_kv, block, n_blocks), i32(n), torch.cuda.Stream()
+    q = rows(batch, n_kv * group, d, seed=3, dtype=BF16).cuda()
+    kc, vc = (rows(n_blocks, n_kv, block, d, seed=s, dtype=BF16).cuda() for s in (1, 2))
+    bd = rows(n_blocks, n_kv, 2, d, seed=4, dtype=BF16).sort(2).values.cuda()
+    scores = tq.block_scores(pages, lens, q, bd)
+    free, one, head = i32(range(n_blocks, n_blocks + 9)), i32([1] * batch), i32([0])
+    ws = tq.attend_paged_workspace_size(pages, max(n), n_kv * group, d)
+    calls = [(lambda st: [tq.block_scores(pages, lens, q, bd, stream=st)], [scores.nbytes]),
+             (lambda st: list(tq.select_blocks(pages, lens, scores, keep, stream=st)), [4 * batch * n_kv * keep, 4 * batch * n_kv]),
+             (lambda st: [tq.attend_paged(pages, lens, max(n), q, kc, vc, stream=st)], [4 * q.numel(), ws]),
+             (lambda st: list(tq.page_extend(pages, lens, one, free, head, n_rows=batch, stream=st)),
+              [8 * batch * n_kv, 4 * batch, 4 * batch, 4, 8 * (batch + 1)])]
+    for call, sizes in calls:
+        want = [x.clone() for x in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        copies = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in sizes]
+        freed = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for size in sizes]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)  # some 0.1 s
+        for c, f in zip(copies, freed):
+            c.copy_(f)
+            f.fill_(255)
+        del freed, f
+        got = call(side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(c.eq(7).all() for c in copies)
+
+
 def test_profiled_calls(tq):
     """Per-kernel timing counts the paged-cache kernels under their names, and the results stay the same."""
     plain = serve(tq, 2, graph=False)[0]

@@ -130,3 +130,31 @@ def test_binding_refuses_host_tensors(lib):
         lib.Pages(torch.zeros(2, 3, dtype=torch.int32), 1, 16, 4)
     with pytest.raises(ValueError):
         lib.Pages(torch.zeros(3, dtype=torch.int32), 1, 16, 4)
+
+
+def test_own_tensors_come_from_the_given_stream(lib, monkeypatch):
+    """A tensor that a call makes for itself belongs to the stream that it works on, and the caller's stream keeps it
+    from reuse.  Streams and tensors are stand-ins: what matters is which stream is current at the allocation."""
+    import contextlib
+    now, made = ["caller"], []
+
+    class Made:
+        def __init__(self):
+            self.of, self.kept_by = now[0], []
+            made.append(self)
+
+        def record_stream(self, s):
+            self.kept_by.append(s)
+
+    @contextlib.contextmanager
+    def switch(s):
+        before, now[0] = now[0], s
+        yield
+        now[0] = before
+
+    monkeypatch.setattr(lib.torch, "empty", lambda *a, **k: Made())
+    monkeypatch.setattr(lib.torch.cuda, "current_stream", lambda device=None: now[0])
+    monkeypatch.setattr(lib.torch.cuda, "stream", switch)
+    for given in (None, "caller", "other"):
+        lib._new((2, 3), lib.torch.int32, "cuda:0", given)
+    assert [(t.of, t.kept_by) for t in made] == [("caller", []), ("caller", []), ("other", ["caller"])] and now == ["caller"]
