@@ -261,11 +261,26 @@ class Packed:
         return p
 
 
-def _workspace(nbytes: int, device: int, ws):
+def _new(shape, dtype, device, stream):
+    """A tensor that a call makes for itself.  On a given stream it comes from that stream's own memory: a block of
+    the current stream's may still be in use by what is queued there, which the given stream does not wait for.  The
+    current stream, where the caller goes on, keeps it from reuse too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _workspace(nbytes: int, device: int, ws, stream):
     if nbytes == 0:
         return c_void_p(None), 0
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+        ws = _new(nbytes, torch.uint8, torch.device("cuda", device), stream)
     return _dev(ws, device, "ws"), ws.numel() * ws.element_size()
 
 
@@ -286,7 +301,7 @@ def encode_kv(ctx: Context, x: torch.Tensor, out: Packed, slots: torch.Tensor = 
         sp = _dev(slots, ctx.device, "slots", torch.int64)
         if slots.numel() != n:
             raise ValueError("slots must have n entries")
-    w, wb = _workspace(encode_workspace_size(ctx, n), ctx.device, ws)
+    w, wb = _workspace(encode_workspace_size(ctx, n), ctx.device, ws, stream)
     _check(LIB.tq_encode_kv(ctx.handle, xp, _dtype_code(x), n, ld, sp, out.c(ctx), w, wb, _stream_ptr(stream)))
     return out
 
@@ -304,10 +319,10 @@ def scores(ctx: Context, q: torch.Tensor, keys: Packed, n: int = None, out=None,
     n = keys.capacity if n is None else n
     nq = q.shape[0]
     if out is None:
-        out = torch.empty(nq, n, dtype=torch.float32, device=q.device)
+        out = _new((nq, n), torch.float32, q.device, stream)
     if tuple(out.shape) != (nq, n):
         raise ValueError("out must be [nq, n]")
-    w, wb = _workspace(scores_workspace_size(ctx, nq), ctx.device, ws)
+    w, wb = _workspace(scores_workspace_size(ctx, nq), ctx.device, ws, stream)
     _check(LIB.tq_scores(ctx.handle, _dev(q, ctx.device, "q"), _dtype_code(q), nq, keys.c(ctx), n,
                          _dev(out, ctx.device, "out", torch.float32), w, wb, _stream_ptr(stream)))
     return out
@@ -361,8 +376,8 @@ def attend_decode(kctx: Context, vctx: Context, q: torch.Tensor, kcache: Packed,
         desc = make_attn_desc(kctx, vctx, tuple(q.shape), kcache, vcache, seq_lens, max_seq_len, ctx_stride,
                               block_table, block_size, scale, n_kv_heads)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    w, wb = _workspace(attend_workspace_size(kctx, vctx, desc), kctx.device, ws)
+        out = _new(q.shape, torch.float32, q.device, stream)
+    w, wb = _workspace(attend_workspace_size(kctx, vctx, desc), kctx.device, ws, stream)
     _check(LIB.tq_attend_decode(kctx.handle, vctx.handle, ctypes.byref(desc), _dev(q, kctx.device, "q"),
                                 _dtype_code(q), _dev(out, kctx.device, "out", torch.float32), w, wb,
                                 _stream_ptr(stream)))
@@ -385,8 +400,8 @@ def decode_step(kctx: Context, vctx: Context, q: torch.Tensor, k_new: torch.Tens
     if new_slots.numel() != n_new:
         raise ValueError("new_slots must have n_new entries")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    w, wb = _workspace(decode_step_workspace_size(kctx, vctx, desc, n_new), kctx.device, ws)
+        out = _new(q.shape, torch.float32, q.device, stream)
+    w, wb = _workspace(decode_step_workspace_size(kctx, vctx, desc, n_new), kctx.device, ws, stream)
     _check(LIB.tq_decode_step(kctx.handle, vctx.handle, ctypes.byref(desc), _dev(k_new, kctx.device, "k_new"),
                               _dev(v_new, kctx.device, "v_new"), _dtype_code(k_new), n_new,
                               _dev(new_slots, kctx.device, "new_slots", torch.int64), _dev(q, kctx.device, "q"),
@@ -454,10 +469,10 @@ def search_topk(ctx: Context, q: torch.Tensor, db: Packed, k: int, n: int = None
     n = db.capacity if n is None else n
     nq = q.shape[0]
     if out_scores is None:
-        out_scores = torch.empty(nq, k, dtype=torch.float32, device=q.device)
+        out_scores = _new((nq, k), torch.float32, q.device, stream)
     if out_idx is None:
-        out_idx = torch.empty(nq, k, dtype=torch.int64, device=q.device)
-    w, wb = _workspace(search_workspace_size(ctx, nq, n, k), ctx.device, ws)
+        out_idx = _new((nq, k), torch.int64, q.device, stream)
+    w, wb = _workspace(search_workspace_size(ctx, nq, n, k), ctx.device, ws, stream)
     _check(LIB.tq_search_topk(ctx.handle, _dev(q, ctx.device, "q"), _dtype_code(q), nq, db.c(ctx), n, k,
                               _dev(out_scores, ctx.device, "out_scores", torch.float32),
                               _dev(out_idx, ctx.device, "out_idx", torch.int64), w, wb, _stream_ptr(stream)))
@@ -470,21 +485,6 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambd
 
 def _raw_stream(device: int, stream) -> int:
     return _current_stream(device) if stream is None else stream.cuda_stream
-
-
-def _new(shape, dtype, device, stream):
-    """A tensor that a call makes for itself.  On a given stream it comes from that stream's own memory: a block of
-    the current stream's may still be in use by what is queued there, which the given stream does not wait for.  The
-    current stream, where the caller goes on, keeps it from reuse too."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    if stream == here:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(here)
-    return t
 
 
 class Pages:

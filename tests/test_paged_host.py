@@ -158,3 +158,16 @@ def test_own_tensors_come_from_the_given_stream(lib, monkeypatch):
     for given in (None, "caller", "other"):
         lib._new((2, 3), lib.torch.int32, "cuda:0", given)
     assert [(t.of, t.kept_by) for t in made] == [("caller", []), ("caller", []), ("other", ["caller"])] and now == ["caller"]
+
+
+def test_no_call_allocates_for_itself_but_on_its_stream(lib):
+    """Every call that makes outputs or workspaces makes them where its stream is heeded."""
+    import ast
+    import inspect
+    for f in ast.walk(ast.parse(inspect.getsource(lib))):
+        if isinstance(f, ast.FunctionDef) and f.name != "_new" and "stream" in [a.arg for a in f.args.args]:
+            made = [n.func.attr for n in ast.walk(f) if isinstance(n, ast.Call) and isinstance(n.func, ast.Attribute)
+                    and isinstance(n.func.value, ast.Name) and n.func.value.id == "torch"]
+            assert not {"empty", "zeros", "full", "empty_like"} & set(made), f.name
+    for name in ("encode_kv", "scores", "attend_decode", "decode_step", "search_topk"):
+        assert "_workspace(" in inspect.getsource(getattr(lib, name)) and ", ws, stream)" in inspect.getsource(getattr(lib, name)), name
