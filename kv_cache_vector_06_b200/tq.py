@@ -281,7 +281,9 @@ def _workspace(nbytes: int, device: int, ws, stream):
         return c_void_p(None), 0
     if ws is None:
         ws = _new(nbytes, torch.uint8, torch.device("cuda", device), stream)
-    return _dev(ws, device, "ws"), ws.numel() * ws.element_size()
+    p = _dev(ws, device, "ws")
+    p.keep = ws  # until the caller's launches are queued: another thread must not be given its memory in between
+    return p, ws.numel() * ws.element_size()
 
 
 def encode_workspace_size(ctx: Context, n: int) -> int:

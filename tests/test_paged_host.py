@@ -171,3 +171,26 @@ def test_no_call_allocates_for_itself_but_on_its_stream(lib):
             assert not {"empty", "zeros", "full", "empty_like"} & set(made), f.name
     for name in ("encode_kv", "scores", "attend_decode", "decode_step", "search_topk"):
         assert "_workspace(" in inspect.getsource(getattr(lib, name)) and ", ws, stream)" in inspect.getsource(getattr(lib, name)), name
+
+
+def test_workspace_lives_until_the_launches_are_queued(lib, monkeypatch):
+    """The address that a call passes on holds the tensor behind it: the library works without the interpreter's
+    lock, and a thread that allocates meanwhile must not be given the same memory."""
+    import gc
+    import weakref
+    import torch
+    seen = []
+
+    def made(*a):
+        t = torch.empty(64, dtype=torch.uint8)
+        seen.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(lib, "_new", made)
+    monkeypatch.setattr(lib, "_dev", lambda t, *a, **k: lib.c_void_p(t.data_ptr()))
+    w, n = lib._workspace(64, 0, None, None)
+    gc.collect()
+    assert n == 64 and seen[0]() is not None and w.value == seen[0]().data_ptr()
+    del w
+    gc.collect()
+    assert seen[0]() is None
