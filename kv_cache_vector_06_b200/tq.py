@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
@@ -489,6 +490,24 @@ def _raw_stream(device: int, stream) -> int:
     return _current_stream(device) if stream is None else stream.cuda_stream
 
 
+@functools.lru_cache(maxsize=256)
+def _same_order(shape, whole) -> bool:
+    """Whether a contiguous array of `shape` holds what one of shape `whole` = (n_blocks, n_kv_heads, rows, d) does, in
+    its order: neighbouring dimensions may be joined, and the blocks split into several dimensions (heads counted
+    among the blocks).  An array with the same number of entries in another order is not."""
+    blocks, allowed, at = whole[0], set(), 1
+    for n in whole:
+        at *= n
+        allowed.add(at)
+    ends, end = set(), 1
+    for n in shape:
+        end *= n
+        ends.add(end)
+    if not shape or shape[-1] != whole[3] or end != at:
+        return False
+    return at == 0 or all(e == 1 or e in allowed or (e < blocks and blocks in ends) for e in ends)
+
+
 class Pages:
     """Paged-cache addressing (tq_pages): the block table [batch, max_blocks] and the cache's shape.
     Holds the table's tensor; the calls below run on its device."""
@@ -501,6 +520,7 @@ class Pages:
         self.block_table = block_table
         self.n_kv_heads, self.block_size, self.n_blocks = n_kv_heads, block_size, n_blocks
         self.rows = self.batch * n_kv_heads
+        self._dims = (n_blocks, n_kv_heads)  # of the caches, whatever heads the sequences have
         self._c = PagesC(self.device if block_table.is_cuda else -1, self.batch, n_kv_heads, block_size, self.max_blocks,
                          n_blocks, _dev(block_table, self.device, "block_table", torch.int32))
         self.ref = ctypes.byref(self._c)
@@ -508,7 +528,9 @@ class Pages:
     def selected(self, sel_table: torch.Tensor) -> "Pages":
         """The same cache as batch * n_kv_heads sequences of one KV head each, over the blocks that
         select_blocks chose."""
-        return Pages(sel_table, 1, self.block_size, self.n_blocks * self.n_kv_heads)
+        p = Pages(sel_table, 1, self.block_size, self.n_blocks * self.n_kv_heads)
+        p._dims = self._dims
+        return p
 
     def _arg(self, t: torch.Tensor, name: str, dtype, shape) -> int:
         """Address of a contiguous tensor of this device with the given type and shape (an int: its number
@@ -521,8 +543,9 @@ class Pages:
 
     def _cache(self, t: torch.Tensor, name: str, per_block: int, d: int, dtype) -> int:
         """Address of an array of `per_block` rows of d per (block, KV head)."""
-        if t.shape[-1] != d:
-            raise ValueError(f"{name} must be [{self.n_blocks}, {self.n_kv_heads}, {per_block}, {d}]")
+        whole = (*self._dims, per_block, d)
+        if t.shape != whole and not _same_order(t.shape, whole):
+            raise ValueError(f"{name} must be {list(whole)} (got {list(t.shape)})")
         return self._arg(t, name, dtype, self.n_blocks * self.n_kv_heads * per_block * d)
 
 

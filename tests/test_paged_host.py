@@ -194,3 +194,55 @@ def test_workspace_lives_until_the_launches_are_queued(lib, monkeypatch):
     del w
     gc.collect()
     assert seen[0]() is None
+
+
+def host_pages(lib, n_kv, block, n_blocks, batch=2, width=4):
+    """Pages of a table in host memory: what the binding checks before it calls the library."""
+    import torch
+    p = object.__new__(lib.Pages)
+    p.device, p.batch, p.max_blocks, p.n_kv_heads, p.block_size, p.n_blocks = -1, batch, width, n_kv, block, n_blocks
+    p._dims = (n_blocks, n_kv)
+    p.rows, p.block_table = batch * n_kv, torch.zeros(batch, width, dtype=torch.int32)
+    p._c = lib.PagesC(-1, batch, n_kv, block, width, n_blocks, p.block_table.data_ptr())
+    p.ref = ctypes.byref(p._c)
+    return p
+
+
+@pytest.mark.parametrize("n_kv,block,shape,fits", [
+    (2, 16, (5, 2, 16, 8), True),
+    (2, 16, (10, 16, 8), True), (2, 16, (5, 32, 8), True), (2, 16, (160, 8), True),  # neighbours joined
+    (1, 16, (5, 2, 16, 8), True),    # ten blocks of one head: the heads counted among the blocks
+    (2, 16, (1, 160, 8), True), (1, 16, (5, 1, 2, 16, 8), True), (1, 16, (10, 16, 1, 8), True), (2, 1, (5, 1, 2, 8), True),
+    (2, 16, (5, 16, 2, 8), False),   # token before head
+    (1, 16, (5, 16, 2, 8), False),
+    (2, 16, (2, 5, 16, 8), False),   # head before block
+    (2, 16, (5, 2, 8, 16), False), (2, 16, (5, 2, 16, 4), False), (2, 16, (6, 2, 16, 8), False),
+    (2, 16, (80, 2, 8), False), (2, 16, (1280,), False), (2, 16, (), False)])
+def test_caches_of_another_order_are_refused(lib, n_kv, block, shape, fits):
+    """An array of as many entries in another order of blocks, heads and tokens is not read as this one."""
+    import torch
+    p = host_pages(lib, n_kv, block, 10 // n_kv)
+    t = torch.zeros(shape)
+    if fits:
+        assert p._cache(t, "k_cache", block, 8, torch.float32) == t.data_ptr()
+    else:
+        with pytest.raises(ValueError, match="k_cache must"):
+            p._cache(t, "k_cache", block, 8, torch.float32)
+
+
+def test_caches_of_selected_pages(lib, monkeypatch):
+    """Pages over chosen blocks take the caches of the pages that they were made from."""
+    import torch
+    monkeypatch.setattr(lib.Pages, "__init__", lambda self, table, h, bs, n: self.__dict__.update(
+        host_pages(lib, h, bs, n, *table.shape).__dict__))
+    p = host_pages(lib, 2, 16, 5).selected(torch.zeros(4, 3, dtype=torch.int32))
+    assert (p.n_kv_heads, p.n_blocks, p.rows) == (1, 10, 4)
+    for shape in ((5, 2, 16, 8), (5, 32, 8), (10, 16, 8), (160, 8)):
+        p._cache(torch.zeros(shape), "k_cache", 16, 8, torch.float32)
+    with pytest.raises(ValueError):
+        p._cache(torch.zeros(5, 16, 2, 8), "k_cache", 16, 8, torch.float32)
+
+
+def test_empty_caches_pass(lib):
+    import torch
+    host_pages(lib, 2, 16, 0)._cache(torch.zeros(0, 2, 16, 8), "k_cache", 16, 8, torch.float32)
