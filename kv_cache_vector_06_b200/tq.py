@@ -585,11 +585,14 @@ def append_kv(pages: Pages, seq_lens, granted, row_offsets, k_new, v_new=None, k
     and row_offsets as page_extend returns them.  Without caches (None) only the bounds are kept."""
     n, h, d = k_new.shape if k_new.dim() == 3 else (0, -1, 0)
     strides, dt, dev, b = k_new.stride(), k_new.dtype, pages.device, pages.batch
-    if h != pages.n_kv_heads or (v_new is not None and (v_new.shape != k_new.shape or v_new.stride() != strides
-                                                        or v_new.dtype is not dt)):
-        raise ValueError(f"k_new and v_new must both be [n_rows, {pages.n_kv_heads}, d] with one dtype and one row stride")
-    if (d > 1 and strides[2] != 1) or (h > 1 and strides[1] != d):
-        raise ValueError("the heads of a row must lie side by side")
+    if h != pages.n_kv_heads or (v_new is not None and (v_new.shape != k_new.shape or v_new.dtype is not dt)):
+        raise ValueError(f"k_new and v_new must both be [n_rows, {pages.n_kv_heads}, d] with one dtype")
+    for s in (strides,) if v_new is None else (strides, v_new.stride()):
+        # the stride of a dimension with one entry says nothing
+        if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+            raise ValueError("the heads of a row must lie side by side")
+        if n > 1 and s[0] != strides[0]:
+            raise ValueError("k_new and v_new must have one row stride")
     if k_new.get_device() != dev or (v_new is not None and v_new.get_device() != dev):
         raise ValueError(f"k_new and v_new must be CUDA tensors on device {dev}")
     arg, cache, i32 = pages._arg, pages._cache, torch.int32

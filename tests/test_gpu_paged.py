@@ -162,6 +162,17 @@ def test_append_one_sequence(tq, granted):
     append_case(tq, [37], granted, 2, 16, 128, BF16, seed=3, n_rows=4)
 
 
+def test_append_one_row_beside_a_joint_projection(tq):
+    """One row: keys from a projection's output, values by themselves, whose row strides differ and do not matter."""
+    n_kv, d, block = 2, 64, 16
+    joint = rows(1, 2, n_kv, d, seed=1, dtype=BF16).cuda()
+    k, v = joint[:, 0], rows(1, n_kv, d, seed=2, dtype=BF16).cuda()
+    assert k.stride(0) != v.stride(0)
+    kc, vc = (torch.zeros(3, n_kv, block, d, dtype=BF16).cuda() for _ in (0, 1))
+    tq.append_kv(tq.Pages(i32([[2]]), n_kv, block, 3), i32([5]), i32([1]), torch.tensor([0, 1]).cuda(), k, v, kc, vc)
+    assert torch.equal(kc[2, :, 4], k[0]) and torch.equal(vc[2, :, 4], v[0]) and kc.count_nonzero() == k.count_nonzero()
+
+
 def test_append_refused_rows_and_bounds_only(tq):
     """Refused sequences keep their rows unread (offsets count them); a sequence whose rows pass n_rows is
     not appended; caches and bounds each without the other; table entries that name no block."""

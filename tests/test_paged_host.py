@@ -246,3 +246,52 @@ def test_caches_of_selected_pages(lib, monkeypatch):
 def test_empty_caches_pass(lib):
     import torch
     host_pages(lib, 2, 16, 0)._cache(torch.zeros(0, 2, 16, 8), "k_cache", 16, 8, torch.float32)
+
+
+class FakeLibrary:
+    """Takes the arguments of tq_append_kv and does nothing."""
+
+    def tq_append_kv(self, *a):
+        self.args = a
+        return OK
+
+
+class FakeStream:
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("n,n_kv,split,ok", [(1, 2, "k", True), (1, 2, "v", True), (1, 1, "k", True), (0, 2, "k", True),
+                                             (3, 1, "both", True), (3, 2, "both", True), (3, 2, "k", False), (3, 2, "v", False),
+                                             (1, 2, "heads", False), (3, 2, "heads", False), (3, 1, "heads", True)])
+def test_append_rows_of_any_stride_that_matters(lib, monkeypatch, n, n_kv, split, ok):
+    """k_new, v_new or both halves of one projection's rows: with one row (or head) their strides along it may
+    differ; with more, they must agree, and heads must lie side by side."""
+    import torch
+    monkeypatch.setattr(lib, "LIB", FakeLibrary())
+    p, d = host_pages(lib, n_kv, 16, 5), 8
+    joint = torch.zeros(n, 2, n_kv, d)
+    k, v = joint[:, 0], joint[:, 1]
+    if split == "heads":  # heads lie apart
+        k = v = torch.zeros(n_kv, n, d).transpose(0, 1) if n > 1 else torch.zeros(n, n_kv, 2, d)[:, :, 0]
+    k, v = k if split != "v" else torch.zeros(k.shape), v if split != "k" else torch.zeros(v.shape)
+    ints = [torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)]
+    kc = torch.zeros(5, n_kv, 16, d)
+    if not ok:
+        with pytest.raises(ValueError):
+            lib.append_kv(p, *ints, k, v, kc, kc.clone(), stream=FakeStream)
+        return
+    lib.append_kv(p, *ints, k, v, kc, kc.clone(), stream=FakeStream)
+    a = lib.LIB.args
+    assert a[4] == k.data_ptr() and a[5] == v.data_ptr() and a[7] == d and a[8] == n
+    assert a[9] == (k.stride(0) if n > 1 else n_kv * d) and a[9] >= n_kv * d
+
+
+def test_append_refuses_other_heads_and_types(lib, monkeypatch):
+    import torch
+    monkeypatch.setattr(lib, "LIB", FakeLibrary())
+    p = host_pages(lib, 2, 16, 5)
+    ints = [torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)]
+    k, kc = torch.zeros(3, 2, 8), torch.zeros(5, 2, 16, 8)
+    for kn, vn in ((k, k.bfloat16()), (k, k[:2]), (torch.zeros(3, 4, 8), torch.zeros(3, 4, 8)), (k[0], k[0])):
+        with pytest.raises(ValueError):
+            lib.append_kv(p, *ints, kn, vn, kc, kc.clone(), stream=FakeStream)
