@@ -464,6 +464,28 @@ def test_attend_workspace_reused(tq):
         check_attend(tq, lens, 2, 4, 16, 128, BF16, seed=20 + seed, ws=ws)
 
 
+def test_attend_workspace_reused_by_shared_rows(tq):
+    """One workspace, filled with NaN, for calls whose rows are all cut into pieces that lie in it: other shapes, head
+    counts and types in a row."""
+    ws = torch.full((1 << 25,), 255, dtype=torch.uint8).cuda()
+    for seed, (lens, group, d, dtype) in enumerate((([9001, 20, 700], 4, 128, BF16), ([12000], 8, 64, F32), ([9500] * 5, 1, 128, F32),
+                                                    ([10000, 0, 1], 16, 64, BF16), ([9001, 20, 700], 4, 128, BF16))):
+        check_attend(tq, lens, 2, group, 16, d, dtype, seed=30 + seed, ws=ws)
+
+
+@pytest.mark.parametrize("dtype,out_dtype,d,group", [
+    (BF16, F32, 64, 1), (BF16, BF16, 64, 16), (BF16, F32, 80, 4), (BF16, BF16, 128, 4), (BF16, F32, 128, 9), (BF16, F32, 192, 5),
+    (BF16, BF16, 256, 8), (BF16, F32, 256, 16), (F32, F32, 64, 4), (F32, F32, 64, 16), (F32, F32, 80, 1), (F32, F32, 128, 4),
+    (F32, F32, 128, 16), (F32, F32, 192, 9), (F32, F32, 256, 4), (F32, F32, 256, 16)])
+def test_attend_many_short_rows(tq, dtype, out_dtype, d, group):
+    """More rows than the GPU has room for, of few steps each, which single warps take; rows of a long one among them
+    are shared by many warps."""
+    rng = np.random.default_rng(d + group)
+    lens = rng.integers(0, 60, 301)
+    lens[rng.integers(0, 301)] = 3001
+    check_attend(tq, lens.tolist(), 3, group, 16, d, dtype, out_dtype=out_dtype, seed=d + group)
+
+
 def test_attend_captured_calls_share_a_workspace(tq):
     """Two captured calls of different shapes and an eager one on one workspace, replayed in turn: the same bits
     every time, whatever the call before left there."""
@@ -616,6 +638,79 @@ def test_serving_steps_on_two_streams(tq):
     for x, y in zip(alone, both):
         for u, w in zip(x, y):
             assert all(torch.equal(a, b) for a, b in zip(u, w))
+
+
+class Serving:
+    """Three sequences over a cache of their own: grow, append, score, choose, attend (rows cut into pieces, and the
+    chosen blocks), every step's results kept."""
+
+    def __init__(self, tq, seed):
+        self.tq, self.n_kv, self.group, self.d, self.block, self.steps = tq, 2, 4, 128, 16, 12
+        held = [20000 + seed, 700, 3000]
+        width = 1300
+        table, used = tables(held, width, self.block, seed)
+        n_blocks = used + 40
+        self.pages = tq.Pages(i32(table), self.n_kv, self.block, n_blocks)
+        self.free, self.head, self.lens = i32(np.arange(used, n_blocks)), i32([0]), i32(held)
+        self.k, self.v = (rows(n_blocks, self.n_kv, self.block, self.d, seed=seed + i, dtype=BF16).cuda() for i in (1, 2))
+        self.bounds = self.k.aminmax(dim=2)
+        self.bounds = torch.stack([self.bounds.min, self.bounds.max], dim=2)
+        self.new = rows(self.steps, 2, 3, self.n_kv, self.d, seed=seed + 3, dtype=BF16).cuda()
+        self.q = rows(self.steps, 3, self.n_kv * self.group, self.d, seed=seed + 4, dtype=BF16).cuda()
+        self.one, self.max_len, self.kept = i32([1, 1, 1]), width * self.block, []
+
+    def step(self, i):
+        tq, keep = self.tq, 40
+        slots, _, granted, _, off = tq.page_extend(self.pages, self.lens, self.one, self.free, self.head, n_rows=3,
+                                                   seq_lens_out=self.lens, free_head_out=self.head)
+        tq.append_kv(self.pages, self.lens, granted, off, self.new[i, 0], self.new[i, 1], self.k, self.v, self.bounds)
+        s = tq.block_scores(self.pages, self.lens, self.q[i], self.bounds)
+        table, held = tq.select_blocks(self.pages, self.lens, s, keep)
+        full = tq.attend_paged(self.pages, self.lens, self.max_len, self.q[i], self.k, self.v)
+        part = tq.attend_paged(self.pages.selected(table), held, keep * self.block, self.q[i].view(3 * self.n_kv, self.group, self.d),
+                               self.k, self.v)
+        self.kept += [slots, s, table, held, full, part]
+
+    def state(self):
+        return self.kept + [self.pages.block_table, self.lens, self.head, self.k, self.v, self.bounds]
+
+
+@pytest.mark.parametrize("threads", [False, True])
+def test_serving_at_once_on_two_streams(tq, threads):
+    """Two caches served at once, every step of both queued before either begins, by one thread in turn or by a thread
+    each: what each gives alone."""
+    import threading
+    seeds, alone = (100, 200), []
+    for s in seeds:
+        alone.append(Serving(tq, s))
+        for i in range(alone[-1].steps):
+            alone[-1].step(i)
+    both, streams = [Serving(tq, s) for s in seeds], [torch.cuda.Stream() for _ in seeds]
+    torch.cuda.synchronize()
+
+    def queue(x, st, some):
+        with torch.cuda.stream(st):
+            for i in some:
+                x.step(i)
+
+    for st in streams:
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(100_000_000)  # some 50 ms: the steps are queued meanwhile
+    if threads:
+        runs = [threading.Thread(target=queue, args=(x, st, range(x.steps))) for x, st in zip(both, streams)]
+        for t in runs:
+            t.start()
+        for t in runs:
+            t.join()
+    else:
+        for i in range(both[0].steps):
+            for x, st in zip(both, streams):
+                queue(x, st, [i])
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        assert len(y.kept) == 6 * x.steps
+        for k, (u, w) in enumerate(zip(x.state(), y.state())):
+            assert torch.equal(u, w), k
 
 
 def test_calls_on_a_given_stream(tq):
