@@ -775,6 +775,39 @@ def test_calls_on_a_given_stream_leave_queued_work_alone(tq):
         assert all(c.eq(7).all() for c in copies)
 
 
+def test_calls_on_a_forked_stream_of_a_capture(tq):
+    """stream= names a stream that joined a capture, not the capturing one: what the calls make for themselves stays
+    the graph's, whatever is allocated between replays."""
+    n_kv, group, d, block = 2, 4, 128, 16
+    n = [20000, 700]
+    table, n_blocks = tables(n, 1250, block, 3)
+    pages, lens, side = tq.Pages(i32(table), n_kv, block, n_blocks), i32(n), torch.cuda.Stream()
+    q = rows(2, n_kv * group, d, seed=3, dtype=BF16).cuda()
+    kc, vc = (rows(n_blocks, n_kv, block, d, seed=s, dtype=BF16).cuda() for s in (1, 2))
+    bd = rows(n_blocks, n_kv, 2, d, seed=4, dtype=BF16).sort(2).values.cuda()
+
+    def run(st):
+        s = tq.block_scores(pages, lens, q, bd, stream=st)
+        t, held = tq.select_blocks(pages, lens, s, 30, stream=st)
+        part = tq.attend_paged(pages.selected(t), held, 30 * block, q.view(2 * n_kv, group, d), kc, vc, stream=st)
+        return [s, t, held, part, tq.attend_paged(pages, lens, max(n), q, kc, vc, stream=st)]
+
+    want = [x.clone() for x in run(None)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = run(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(3):
+        other = [torch.full((1 << (8 + k),), 255, dtype=torch.uint8, device="cuda") for k in range(18)]
+        for x in got:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and all(x.eq(255).all() for x in other)
+
+
 def test_profiled_calls(tq):
     """Per-kernel timing counts the paged-cache kernels under their names, and the results stay the same."""
     plain = serve(tq, 2, graph=False)[0]
