@@ -544,9 +544,11 @@ class Pages:
     def _cache(self, t: torch.Tensor, name: str, per_block: int, d: int, dtype) -> int:
         """Address of an array of `per_block` rows of d per (block, KV head)."""
         whole = (*self._dims, per_block, d)
-        if t.shape != whole and not _same_order(t.shape, whole):
-            raise ValueError(f"{name} must be {list(whole)} (got {list(t.shape)})")
-        return self._arg(t, name, dtype, self.n_blocks * self.n_kv_heads * per_block * d)
+        if (isinstance(t, torch.Tensor) and t.get_device() == self.device and t.dtype is dtype and t.is_contiguous()
+                and (t.shape == whole or _same_order(t.shape, whole))):
+            return t.data_ptr()
+        _dev(t, self.device, name, dtype)
+        raise ValueError(f"{name} must be {list(whole)} (got {list(t.shape)})")
 
 
 def page_extend(pages: Pages, seq_lens, new_lens, free_blocks, free_head, n_rows: int = None, new_slots=None,
@@ -587,12 +589,12 @@ def append_kv(pages: Pages, seq_lens, granted, row_offsets, k_new, v_new=None, k
     strides, dt, dev, b = k_new.stride(), k_new.dtype, pages.device, pages.batch
     if h != pages.n_kv_heads or (v_new is not None and (v_new.shape != k_new.shape or v_new.dtype is not dt)):
         raise ValueError(f"k_new and v_new must both be [n_rows, {pages.n_kv_heads}, d] with one dtype")
-    for s in (strides,) if v_new is None else (strides, v_new.stride()):
-        # the stride of a dimension with one entry says nothing
-        if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-            raise ValueError("the heads of a row must lie side by side")
-        if n > 1 and s[0] != strides[0]:
-            raise ValueError("k_new and v_new must have one row stride")
+    # the stride of a dimension with one entry says nothing
+    v_strides = strides if v_new is None else v_new.stride()
+    if (d > 1 and (strides[2] != 1 or v_strides[2] != 1)) or (h > 1 and (strides[1] != d or v_strides[1] != d)):
+        raise ValueError("the heads of a row must lie side by side")
+    if n > 1 and v_strides[0] != strides[0]:
+        raise ValueError("k_new and v_new must have one row stride")
     if k_new.get_device() != dev or (v_new is not None and v_new.get_device() != dev):
         raise ValueError(f"k_new and v_new must be CUDA tensors on device {dev}")
     arg, cache, i32 = pages._arg, pages._cache, torch.int32
