@@ -314,8 +314,8 @@ tq_status tq_search_topk(const tq_ctx *ctx, const void *q, tq_dtype dtype, int32
 /* ---------------------------------------------------------------------------------------------
  * Paged caches: what a serving loop runs around them.  tq_page_extend makes block tables, lengths
  * and slot maps on the GPU (the `slots` of tq_encode_kv, the `new_slots` of tq_decode_step);
- * tq_append_kv, tq_block_scores and tq_attend_paged serve an uncompressed paged cache (the layers
- * that a user keeps in full precision, [ZC] "Boundary V"); tq_block_scores and
+ * tq_append_kv, tq_block_scores and tq_attend_paged serve an uncompressed paged cache (layers that a
+ * user does not compress; the pages describe none of this); tq_block_scores and
  * tq_select_blocks choose the blocks that one decode step reads, for tq_attend_paged and for
  * tq_attend_decode over the compressed cache alike.
  *
@@ -394,6 +394,8 @@ tq_status tq_append_kv(const tq_pages *pages, const int32_t *seq_lens, const int
  * entries that name no block.
  *   q       device [batch][n_q_heads][d] of dtype
  *   bounds  device, as kept by tq_append_kv
+ * Sums are fp32, and the bound holds to their rounding (some 1e-7 of the absolute terms).  Infinite bounds give
+ * undefined scores, not the same ones for both types.
  *   scores  device fp32 [batch * n_kv_heads][max_blocks]
  * d a multiple of 8 in [8, 256]; n_q_heads / n_kv_heads in [1, 16].
  * Errors: TQ_EINVAL (nulls, shapes, alignment), TQ_EUNSUPPORTED (sizes), TQ_ECUDA. */
@@ -427,7 +429,9 @@ tq_status tq_select_blocks(const tq_pages *pages, const int32_t *seq_lens, const
  *   q            device [batch][n_q_heads][d] of dtype
  *   k_cache, v_cache  device [n_blocks][n_kv_heads][block_size][d] of dtype
  *   scale        0 = 1/sqrt(d)
- *   out          device [batch][n_q_heads][d] of out_dtype: TQ_F32, or dtype
+ *   out          device [batch][n_q_heads][d] of out_dtype: TQ_F32, or dtype.  Sums and the softmax's statistics are
+ *                fp32; its weights enter the products to 2^-17 for a bf16 out, to 2^-25 for an fp32 out of a bf16
+ *                cache, and products over an fp32 cache are off by less than 2^-19 of |x y|
  *   ws           device workspace of tq_attend_paged_workspace_size() bytes, 16-byte aligned; its
  *                contents do not matter, calls that overlap on the GPU need one each
  * d a multiple of 8 in [8, 256]; n_q_heads / n_kv_heads in [1, 16].

@@ -6,7 +6,8 @@
 
 // Rows of d padded to D channels; T the cache's type.  A step's keys and values take 4 to 16 KB of ring.  At
 // least two blocks share an SM, so that one streams while the other begins a row or joins its warps, with
-// two to three steps of each warp in flight and as many registers as the tiles need.  Measured (32 sequences of
+// one (256 channels) to three (64 channels, bf16) steps of each warp in flight beside the one that it works on, and
+// as many registers as the tiles need.  Measured (32 sequences of
 // up to 2000 tokens x 8 heads of 256 channels, bf16): 3 warps x 2 blocks 58 us, 6 x 1 69 us; (up to 4000
 // tokens of 128 channels) 4 x 2 50 us, 8 x 1 58 us, 3 x 3 54 us, two stages instead of three 52 us; (up to
 // 8000 of 64) 4 x 3 51 us, 4 x 2 54 us; (7 x 9999 tokens of 64, fp32) 4 x 2 24.7 us, 4 x 3
@@ -165,7 +166,8 @@ cudaError_t tq_launch_dependent(void (*kern)(P...), dim3 grid, int threads, size
   return tq_launch_clusters(kern, 1, grid, threads, smem, st, args...);
 }
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1: q = (mulhi(n, mul) + n) >> shift with
+// Division of 0 <= n < 2^31 by a fixed d >= 1 (Granlund and Montgomery's method):
+// q = (mulhi(n, mul) + n) >> shift with
 // mul = floor(2^32 (2^shift - d) / d) + 1, shift = ceil(log2 d).
 struct FastDiv {
   uint32_t mul, shift;

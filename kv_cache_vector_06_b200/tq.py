@@ -5,6 +5,9 @@ device pointers, checks that they live on the right device with the right dtype 
 allocates workspaces with torch when the caller gives none, and raises on a non-zero status.
 There is no CPU fallback: if libtq.so is missing or cannot be loaded, importing this module
 raises.
+
+`stream` names the stream that a call's work is queued on (default: the current one).  Ordering the arguments'
+other uses with it is the caller's; outputs and workspaces that a call makes for itself belong to that stream.
 """
 from __future__ import annotations
 
